@@ -451,6 +451,144 @@ MOE_API moe_status moe_backward(const moe_problem *p, const moe_bf16 *x, const m
                                 moe_bf16 *dW1, moe_bf16 *dW2, void *ws, size_t ws_bytes,
                                 void *stream);
 
+/* The layer with a supplied routing: moe_forward without its router, for routings made by
+ * moe_route_select or by the caller. topk_idx [T, k] int32, topk_w [T, k] fp32; a token's
+ * experts are distinct. Dispatch, experts and combine as in moe_forward (the same launches,
+ * less the router's; never the whole-layer launch). An id outside [0, E) or an expert given twice
+ * for one token is reported as MOE_ERR_DEVICE_BAD_INDEX through moe_get_device_status; an id outside
+ * [0, E) contributes nothing to its token. shared: NULL, or the shared expert of
+ * moe_forward_shared (workspace moe_workspace_size_shared). p->gate is not used. */
+MOE_API moe_status moe_forward_routed(const moe_problem *p, const moe_bf16 *x, const int32_t *topk_idx,
+                                      const float *topk_w, const moe_bf16 *W1, const moe_bf16 *W2,
+                                      const moe_shared_expert *shared, moe_bf16 *out, void *ws,
+                                      size_t ws_bytes, void *stream);
+
+/* Backward of moe_forward_routed (without a shared expert): for dout [T, H] bf16, with the routing
+ * as supplied, dx [T, H] bf16 (through the experts only), dtopk_w [T, k] fp32 = dL/dtopk_w (for
+ * moe_route_select_backward), dW1 and dW2 bf16. Shapes, precision and workspace as moe_backward
+ * (moe_backward_workspace_size; p->gate other than MOE_GATE_SOFTMAX_ALL). A pair whose id is outside
+ * [0, E) has gradient 0 and is reported as in moe_forward_routed. */
+MOE_API moe_status moe_backward_routed(const moe_problem *p, const moe_bf16 *x, const int32_t *topk_idx,
+                                       const float *topk_w, const moe_bf16 *W1, const moe_bf16 *W2,
+                                       const moe_bf16 *dout, moe_bf16 *dx, float *dtopk_w, moe_bf16 *dW1,
+                                       moe_bf16 *dW2, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Operators around the layer (beyond the pages): routing by scores, the dense product with a
+ * fused epilogue, dropout with the residual. Conventions as above; the current device must be the
+ * device of the stream and of every pointer.
+ * --------------------------------------------------------------------------------------- */
+
+/* Element types of the operators' tensors. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+
+/* Routing by scores of given logits [T, E] (for instance moe_linear_forward's fp32 output).
+ *   score     s_e = softmax over the token's logits, or 1 / (1 + exp(-l_e)). A logit of -inf or NaN
+ *             masks its expert (score 0; +inf counts as the largest finite value);
+ *   bias      [E] fp32 or NULL, added to the scores for the selection only (balance);
+ *   groups    the experts form n_group groups of E / n_group consecutive ones; a group's value is its
+ *             largest s + bias (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_SUM2); only
+ *             the top_group best groups' experts can be selected, ties to the lower group. n_group =
+ *             top_group = 1 for no groups;
+ *   selection the top_k largest s + bias, ties to the lower id, in that order, as 64-bit
+ *             arithmetic decides it (without a bias: the order of the logits). A -inf or NaN sum (by the
+ *             bias) counts as the lowest key; masked experts come after every other expert of the
+ *             groups that stay, by id, and weigh 0, so every token has top_k distinct ids;
+ *   weights   w_j = scale * s_j / sum of the selected s (renorm != 0; 0 where all are masked), or
+ *             scale * s_j.
+ * Supported: E <= 1024, top_k <= 32, n_group <= 32 dividing E, top_k <= top_group * E / n_group,
+ * 0 < scale < 3e38. ld: elements from one row of logits to the next (0: E). */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_SUM2 1
+typedef struct {
+    int32_t T, E, top_k;
+    int32_t score;       /* MOE_SCORE_* */
+    int32_t n_group, top_group;
+    int32_t group_score; /* MOE_GROUP_* */
+    int32_t renorm;
+    int32_t dtype;       /* type of the logits (and of dlogits): MOE_DTYPE_* */
+    float scale;
+    int64_t ld;
+} moe_select;
+
+/* topk_idx [T, k] int32, topk_w [T, k] fp32 (out). n_rows: NULL, or a device int32; rows from
+ * *n_rows on are not routed and their outputs are left as they were. One launch, no workspace. The
+ * logits' rows need no alignment beyond their type's (16-byte aligned rows are read faster). */
+MOE_API moe_status moe_route_select(const moe_select *s, const void *logits, const float *bias,
+                                    int32_t *topk_idx, float *topk_w, const int32_t *n_rows,
+                                    void *stream);
+
+/* dlogits [T, E] (dense rows, the logits' type) = dL/dlogits for dtopk_w = dL/dtopk_w, the selection
+ * held fixed (it is piecewise constant, so the bias has no gradient). topk_idx as moe_route_select
+ * returned it; an id outside [0, E) is skipped. Masked experts have gradient 0. n_group, top_group and
+ * group_score are checked but not used. One launch, no workspace. */
+MOE_API moe_status moe_route_select_backward(const moe_select *s, const void *logits,
+                                             const int32_t *topk_idx, const float *dtopk_w,
+                                             void *dlogits, const int32_t *n_rows, void *stream);
+
+/* Dense product with its epilogue: z = x W + bias, y = act(z) + residual.
+ *   x [M, K] bf16; W bf16, [K, C] (MOE_W_KN) or [C, K] (MOE_W_NK), with C = 2N for MOE_ACT_SWIGLU
+ *   (columns [0, N) gate, [N, 2N) up, y = silu(gate) * up + residual) and C = N otherwise;
+ *   bias [C] fp32 or NULL (16-byte aligned); residual [M, N] bf16 or NULL; y [M, N] of out_dtype;
+ *   z [M, C] bf16 or NULL: the pre-activation, for moe_linear_backward.
+ * fp32 accumulation and epilogue, one rounding of y (and one of z). N % 8 == 0, K % 8 == 0; M any.
+ * ld*: elements from one row to the next (0: dense), each row start 16-byte aligned. residual may be y
+ * when both are bf16 with the same strides. */
+#define MOE_W_KN 0
+#define MOE_W_NK 1
+typedef struct {
+    int32_t M, N, K;
+    int32_t act;       /* moe_act */
+    int32_t w_layout;  /* MOE_W_* */
+    int32_t out_dtype; /* type of y (and of dy): MOE_DTYPE_* */
+    int64_t ldx, ldw, ldr, ldy, ldz; /* x, W, residual, y (dy), z */
+} moe_linear;
+
+/* Workspace bytes of one call (0 if *p is invalid or unsupported); the status word of
+ * moe_get_device_status is at its start. Calls that run at the same time need one each. */
+MOE_API size_t moe_linear_workspace_size(const moe_linear *p);
+MOE_API size_t moe_linear_backward_workspace_size(const moe_linear *p);
+
+/* One launch: persistent tiles, or, where few tiles would leave SMs idle (small M, few columns),
+ * tiles split along K over clusters of blocks that add their parts in a fixed order. */
+MOE_API moe_status moe_linear_forward(const moe_linear *p, const moe_bf16 *x, const moe_bf16 *W,
+                                      const float *bias, const moe_bf16 *residual, void *y, moe_bf16 *z,
+                                      void *ws, size_t ws_bytes, void *stream);
+
+/* dz = dy act'(z); dx [M, K] = dz W^T, dW = x^T dz in W's layout (both dense, bf16), dbias [C] fp32 =
+ * column sums of dz. dy [M, N] of out_dtype with row stride ldy. Any of dx, dW, dbias may be NULL (not
+ * wanted), not all. z: as moe_linear_forward wrote it (not used, may be NULL, for MOE_ACT_IDENTITY). The
+ * residual's gradient is dy itself. dz is rounded to bf16 for the products; dbias sums it unrounded,
+ * in fp32, in a fixed order. Up to four launches. */
+MOE_API moe_status moe_linear_backward(const moe_linear *p, const moe_bf16 *x, const moe_bf16 *W,
+                                       const moe_bf16 *z, const void *dy, moe_bf16 *dx, moe_bf16 *dW,
+                                       float *dbias, void *ws, size_t ws_bytes, void *stream);
+
+/* Tile plan of later moe_linear_* launches (a test and tuning hook; not thread-safe): tile_n 0 (the
+ * default) picks by an estimate; else tile_n columns with splits 0 (persistent; tile_n 128 or 256) or
+ * splits 1, 2, 4 or 8 blocks per tile along K (tile_n 64 or 128). A plan that a problem cannot take
+ * (SwiGLU with tile_n 64, more splits than 64-value blocks of K) falls back to tile_n 256, splits 0.
+ * The plans differ in the order of the fp32 sums only. Returns 0, or -1 for an unknown plan. */
+MOE_API int moe_set_linear_plan(int tile_n, int splits);
+
+/* Dropout with the residual: y_i = residual_i + (kept ? x_i / (1 - p) : 0) over n elements, with the
+ * drop probability p = drop / 65536 (0 <= drop <= 65536; all dropped at 65536). The mask comes
+ * from a counter-based generator (ten rounds of the 4 x 32-bit generator of Salmon, Moraes, Dror
+ * and Shaw, 2011; 16 bits an element, counter rng[1] + i / 8, key rng[0]) and is not stored. rng: 2
+ * uint64 on the DEVICE (seed, offset), read by the kernel, so a captured call follows them; a call
+ * uses (n + 7) / 8 counters. x, residual (may be NULL), y: dtype, 16-byte aligned, dense; y may be x
+ * or residual. A dropped x does not reach y, whatever its value. */
+MOE_API moe_status moe_dropout_add(int64_t n, int32_t dtype, int32_t drop, const uint64_t *rng,
+                                   const void *x, const void *residual, void *y, void *stream);
+
+/* dx_i = kept ? dy_i / (1 - p) : 0, with the mask of the forward call that used the same rng values.
+ * The residual's gradient is dy. dx may be dy. */
+MOE_API moe_status moe_dropout_add_backward(int64_t n, int32_t dtype, int32_t drop, const uint64_t *rng,
+                                            const void *dy, void *dx, void *stream);
+
 /* Combine (§2.1: gather and reduce the top-k outputs).
  *   out[t][n] = bf16_rne( sum_{j=0..k-1} ys[inv_pos[t][j]][n] ), fp32 sum, j ascending.
  * ys [ys_rows, H] bf16 holds expert-sorted rows that already carry their gate weight;

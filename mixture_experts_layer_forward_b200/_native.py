@@ -75,6 +75,51 @@ class EpRank(ctypes.Structure):
                 ("buf", (ctypes.c_void_p * EP_MAX_WORLD) * len(EP_BUFFERS))]
 
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_SUM2 = 0, 1
+W_KN, W_NK = 0, 1
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _dtype_code(dtype):
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    return _DTYPES[dtype]
+
+
+class Select(ctypes.Structure):
+    """moe_select: routing by scores. The logits' type is taken from the tensors of each call."""
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
+                ("top_group", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("ld", ctypes.c_int64)]
+
+    @classmethod
+    def make(cls, T, E, top_k, score=SCORE_SIGMOID, n_group=1, top_group=1, group_score=GROUP_MAX,
+             renorm=True, scale=1.0):
+        return cls(T, E, top_k, score, n_group, top_group, group_score, 1 if renorm else 0, 0,
+                   scale, 0)
+
+
+class Linear(ctypes.Structure):
+    """moe_linear: y [M, N] = act(x [M, K] W + bias) + residual. The row strides are taken from the
+    tensors of each call."""
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("w_layout", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldz", ctypes.c_int64)]
+
+    @classmethod
+    def make(cls, M, N, K, act=ACT_IDENTITY, w_layout=W_KN, out_dtype=torch.bfloat16):
+        return cls(M, N, K, act, w_layout, _dtype_code(out_dtype), 0, 0, 0, 0, 0)
+
+    @property
+    def cols(self):
+        """Columns of W (and of bias, z): 2N for SwiGLU, else N."""
+        return 2 * self.N if self.act == ACT_SWIGLU else self.N
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -95,7 +140,7 @@ def library() -> ctypes.CDLL:
                 f"g.build()'` (nvcc, sm_100a). There is no CPU fallback.")
         lib = ctypes.CDLL(str(LIB_PATH))
         vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64
-        P = ctypes.POINTER(Problem)
+        P, S, D = ctypes.POINTER(Problem), ctypes.POINTER(Select), ctypes.POINTER(Linear)
         sig = {
             "moe_workspace_size": ([P], sz),
             "moe_forward_launches": ([P], i32),
@@ -138,6 +183,18 @@ def library() -> ctypes.CDLL:
             "moe_ep_buffer_sizes": ([P, i32, ctypes.POINTER(ctypes.c_int64)], i32),
             "moe_ep_workspace_size": ([P, i32], sz),
             "moe_ep_layer_forward": ([ctypes.POINTER(EpRank), i32, vp], i32),
+            "moe_forward_routed": ([P, vp, vp, vp, vp, vp, ctypes.POINTER(SharedExpert), vp, vp, sz,
+                                    vp], i32),
+            "moe_backward_routed": ([P] + [vp] * 11 + [sz, vp], i32),
+            "moe_route_select": ([S] + [vp] * 6, i32),
+            "moe_route_select_backward": ([S] + [vp] * 6, i32),
+            "moe_linear_workspace_size": ([D], sz),
+            "moe_linear_backward_workspace_size": ([D], sz),
+            "moe_linear_forward": ([D] + [vp] * 7 + [sz, vp], i32),
+            "moe_linear_backward": ([D] + [vp] * 8 + [sz, vp], i32),
+            "moe_set_linear_plan": ([i32, i32], i32),
+            "moe_dropout_add": ([i64, i32, i32] + [vp] * 5, i32),
+            "moe_dropout_add_backward": ([i64, i32, i32] + [vp] * 4, i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(lib, name)
@@ -588,3 +645,216 @@ def moe_ep_layer_forward(ranks, stream=None):
     arr = (EpRank * n)(*ranks)
     rc = library().moe_ep_layer_forward(arr, n, _stream(stream))
     _check("moe_ep_layer_forward", rc)
+
+
+# ---------------------------------------------------------------------------------------
+# operators around the layer: routing by scores, the dense product, dropout with the residual
+# ---------------------------------------------------------------------------------------
+
+class _Call:
+    """Checks of one call's tensors: type, shape, rows dense inside, all on one CUDA device that
+    is the current one (the launch goes to the current device's stream)."""
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def rows(self, t, dtype, shape, name, strided=False):
+        """Address and row stride of a tensor (None: 0, 0). strided: rows may be apart."""
+        if t is None:
+            return None, 0
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        device = t.get_device()
+        if device < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if self.device is None:
+            self.device = device
+            if device != torch.cuda.current_device():
+                raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
+        elif device != self.device:
+            raise ValueError(f"{name} is on cuda:{device}, other tensors on cuda:{self.device}")
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        if not strided or t.stride(-1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must be contiguous" + (" within its rows" if strided else ""))
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+
+    def stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if isinstance(stream, torch.cuda.Stream):
+            if self.device is not None and stream.device_index != self.device:
+                raise ValueError("stream is not on the tensors' device")
+            return stream.cuda_stream
+        return int(stream)
+
+
+def _route_dtype(logits):
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    return _dtype_code(logits.dtype)
+
+
+def _select_with(s, dtype, ld):
+    return Select(s.T, s.E, s.top_k, s.score, s.n_group, s.top_group, s.group_score, s.renorm, dtype,
+                  s.scale, ld)
+
+
+def moe_route_select(s: Select, logits, bias, topk_idx, topk_w, n_rows=None, stream=None):
+    """Routing by scores: logits [T, E] float32 or bfloat16 (rows may be apart), bias [E] float32
+    or None -> topk_idx [T, k] int32, topk_w [T, k] float32. n_rows: a CUDA int32 tensor; rows from
+    n_rows[0] on are left as they are."""
+    c = _Call()
+    dt, i32, f32 = _route_dtype(logits), torch.int32, torch.float32
+    lp, ld = c.rows(logits, logits.dtype, (s.T, s.E), "logits", strided=True)
+    rc = library().moe_route_select(
+        _select_with(s, dt, ld), lp, c.rows(bias, f32, (s.E,), "bias")[0],
+        c.rows(topk_idx, i32, (s.T, s.top_k), "topk_idx")[0],
+        c.rows(topk_w, f32, (s.T, s.top_k), "topk_w")[0],
+        c.rows(n_rows, i32, (1,), "n_rows")[0], c.stream(stream))
+    _check("moe_route_select", rc)
+
+
+def moe_route_select_backward(s: Select, logits, topk_idx, dtopk_w, dlogits, n_rows=None,
+                              stream=None):
+    """dlogits [T, E] (the logits' type) from dtopk_w [T, k] float32, the selection held fixed."""
+    c = _Call()
+    dt, i32, f32 = _route_dtype(logits), torch.int32, torch.float32
+    lp, ld = c.rows(logits, logits.dtype, (s.T, s.E), "logits", strided=True)
+    rc = library().moe_route_select_backward(
+        _select_with(s, dt, ld), lp, c.rows(topk_idx, i32, (s.T, s.top_k), "topk_idx")[0],
+        c.rows(dtopk_w, f32, (s.T, s.top_k), "dtopk_w")[0],
+        c.rows(dlogits, logits.dtype, (s.T, s.E), "dlogits")[0],
+        c.rows(n_rows, i32, (1,), "n_rows")[0], c.stream(stream))
+    _check("moe_route_select_backward", rc)
+
+
+def moe_linear_workspace_size(p: Linear) -> int:
+    """Workspace bytes of moe_linear_forward (0: invalid or unsupported)."""
+    return int(library().moe_linear_workspace_size(p))
+
+
+def moe_linear_backward_workspace_size(p: Linear) -> int:
+    """Workspace bytes of moe_linear_backward (0: invalid or unsupported)."""
+    return int(library().moe_linear_backward_workspace_size(p))
+
+
+def _out_dtype(p):
+    return torch.float32 if p.out_dtype == 1 else torch.bfloat16
+
+
+def _w_shape(p):
+    return (p.K, p.cols) if p.w_layout == W_KN else (p.cols, p.K)
+
+
+def moe_linear_forward(p: Linear, x, W, bias, residual, y, ws, z=None, stream=None):
+    """y = act(x W + bias) + residual; z (bfloat16, optional) receives the pre-activation. x, W,
+    residual, y and z may have rows apart (16-byte aligned); bias float32 [p.cols] or None."""
+    c, bf = _Call(), torch.bfloat16
+    xp, ldx = c.rows(x, bf, (p.M, p.K), "x", strided=True)
+    wp, ldw = c.rows(W, bf, _w_shape(p), "W", strided=True)
+    rp, ldr = c.rows(residual, bf, (p.M, p.N), "residual", strided=True)
+    yp, ldy = c.rows(y, _out_dtype(p), (p.M, p.N), "y", strided=True)
+    zp, ldz = c.rows(z, bf, (p.M, p.cols), "z", strided=True)
+    n = ws.numel()
+    rc = library().moe_linear_forward(
+        Linear(p.M, p.N, p.K, p.act, p.w_layout, p.out_dtype, ldx, ldw, ldr, ldy, ldz), xp, wp,
+        c.rows(bias, torch.float32, (p.cols,), "bias")[0], rp, yp, zp,
+        c.rows(ws, torch.uint8, (n,), "ws")[0], n, c.stream(stream))
+    _check("moe_linear_forward", rc)
+
+
+def moe_linear_backward(p: Linear, x, W, z, dy, dx, dW, dbias, ws, stream=None):
+    """dx [M, K], dW (W's layout) bfloat16 and dbias [p.cols] float32 (each may be None: not
+    wanted) from dy [M, N] and the z that moe_linear_forward wrote (None for ACT_IDENTITY)."""
+    c, bf = _Call(), torch.bfloat16
+    xp, ldx = c.rows(x, bf, (p.M, p.K), "x", strided=True)
+    wp, ldw = c.rows(W, bf, _w_shape(p), "W", strided=True)
+    zp, ldz = c.rows(z, bf, (p.M, p.cols), "z", strided=True)
+    dyp, ldy = c.rows(dy, _out_dtype(p), (p.M, p.N), "dy", strided=True)
+    n = ws.numel()
+    rc = library().moe_linear_backward(
+        Linear(p.M, p.N, p.K, p.act, p.w_layout, p.out_dtype, ldx, ldw, 0, ldy, ldz), xp, wp, zp, dyp,
+        c.rows(dx, bf, (p.M, p.K), "dx")[0], c.rows(dW, bf, _w_shape(p), "dW")[0],
+        c.rows(dbias, torch.float32, (p.cols,), "dbias")[0], c.rows(ws, torch.uint8, (n,), "ws")[0], n,
+        c.stream(stream))
+    _check("moe_linear_backward", rc)
+
+
+def moe_set_linear_plan(tile_n: int, splits: int) -> None:
+    """Tile plan of later moe_linear_* launches (a test and tuning hook; tile_n 0: automatic)."""
+    if int(library().moe_set_linear_plan(int(tile_n), int(splits))) < 0:
+        raise ValueError(f"unknown linear plan ({tile_n}, {splits})")
+
+
+def _drop(prob):
+    """The drop probability in 65536ths, as the library takes it."""
+    if not 0.0 <= prob <= 1.0:
+        raise ValueError(f"prob must be in [0, 1], got {prob}")
+    return int(round(prob * 65536))
+
+
+def moe_dropout_add(x, residual, y, prob: float, rng, stream=None):
+    """y = residual + dropout(x): x, residual (or None), y of one shape and type (bfloat16 or
+    float32); prob is rounded to a multiple of 2^-16; rng: CUDA int64 tensor (seed, offset); the call uses ceil(x.numel() / 8) counters of
+    it. The mask is never stored: moe_dropout_add_backward forms it again from the same rng."""
+    c, dt = _Call(), _route_dtype(x)
+    rc = library().moe_dropout_add(
+        x.numel(), dt, _drop(prob), c.rows(rng, torch.int64, (2,), "rng")[0],
+        c.rows(x, x.dtype, x.shape, "x")[0], c.rows(residual, x.dtype, x.shape, "residual")[0],
+        c.rows(y, x.dtype, x.shape, "y")[0], c.stream(stream))
+    _check("moe_dropout_add", rc)
+
+
+def moe_dropout_add_backward(dy, dx, prob: float, rng, stream=None):
+    """dx = dropout's gradient of dy, with the mask of the forward call that used these rng values
+    (the residual's gradient is dy)."""
+    c, dt = _Call(), _route_dtype(dy)
+    rc = library().moe_dropout_add_backward(
+        dy.numel(), dt, _drop(prob), c.rows(rng, torch.int64, (2,), "rng")[0],
+        c.rows(dy, dy.dtype, dy.shape, "dy")[0], c.rows(dx, dy.dtype, dy.shape, "dx")[0],
+        c.stream(stream))
+    _check("moe_dropout_add_backward", rc)
+
+
+def moe_forward_routed(p, x, topk_idx, topk_w, W1, W2, out, ws, shared=None, stream=None):
+    """The layer with a supplied routing (topk_idx [T, k] int32, topk_w [T, k] float32, for
+    instance moe_route_select's). shared: None or (W1s, W2s, w_sg), as moe_forward_shared takes
+    them (workspace moe_workspace_size_shared)."""
+    c, bf = _Call(), torch.bfloat16
+    w1c = 2 * p.F if p.act == ACT_SWIGLU else p.F
+    sh = None
+    if shared is not None:
+        W1s, W2s, w_sg = shared
+        fs = int(W2s.shape[0])
+        sh = SharedExpert(fs, c.rows(W1s, bf, (p.H, 2 * fs), "W1s")[0],
+                          c.rows(W2s, bf, (fs, p.H), "W2s")[0], c.rows(w_sg, bf, (p.H,), "w_sg")[0])
+    n = ws.numel()
+    rc = library().moe_forward_routed(
+        p, c.rows(x, bf, (p.T, p.H), "x")[0], c.rows(topk_idx, torch.int32, (p.T, p.top_k), "topk_idx")[0],
+        c.rows(topk_w, torch.float32, (p.T, p.top_k), "topk_w")[0],
+        c.rows(W1, bf, (p.E, p.H, w1c), "W1")[0], c.rows(W2, bf, (p.E, p.F, p.H), "W2")[0], sh,
+        c.rows(out, bf, (p.T, p.H), "out")[0], c.rows(ws, torch.uint8, (n,), "ws")[0], n,
+        c.stream(stream))
+    _check("moe_forward_routed", rc)
+
+
+def moe_backward_routed(p, x, topk_idx, topk_w, W1, W2, dout, dx, dtopk_w, dW1, dW2, ws, stream=None):
+    """Gradients of moe_forward_routed (no shared expert): dx, dW1, dW2 bfloat16 and dtopk_w [T, k]
+    float32, for moe_route_select_backward. Workspace: moe_backward_workspace_size."""
+    c, bf, f32 = _Call(), torch.bfloat16, torch.float32
+    w1c = 2 * p.F if p.act == ACT_SWIGLU else p.F
+    w1s, w2s, xs, ks = (p.E, p.H, w1c), (p.E, p.F, p.H), (p.T, p.H), (p.T, p.top_k)
+    n = ws.numel()
+    rc = library().moe_backward_routed(
+        p, c.rows(x, bf, xs, "x")[0], c.rows(topk_idx, torch.int32, ks, "topk_idx")[0],
+        c.rows(topk_w, f32, ks, "topk_w")[0], c.rows(W1, bf, w1s, "W1")[0],
+        c.rows(W2, bf, w2s, "W2")[0], c.rows(dout, bf, xs, "dout")[0], c.rows(dx, bf, xs, "dx")[0],
+        c.rows(dtopk_w, f32, ks, "dtopk_w")[0], c.rows(dW1, bf, w1s, "dW1")[0],
+        c.rows(dW2, bf, w2s, "dW2")[0], c.rows(ws, torch.uint8, (n,), "ws")[0], n, c.stream(stream))
+    _check("moe_backward_routed", rc)

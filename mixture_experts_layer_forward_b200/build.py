@@ -1,7 +1,8 @@
 """Build the CUDA shared library (sm_100a) in-tree with nvcc.
 
-The library is one translation unit (csrc/moe_api.cu includes the kernel headers) and
-exports the C ABI declared in include/moe.h.
+The library has two translation units: csrc/moe_api.cu (the layer) and csrc/ops_api.cu (the
+operators around it), which include the kernel headers; together they export the C ABI
+declared in include/moe.h.
 """
 from __future__ import annotations
 
@@ -19,9 +20,10 @@ LIB_PATH = PKG / "libmoe_b200.so"
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-Xcompiler", "-fvisibility=hidden",
 ]
+UNITS = ("moe_api.cu", "ops_api.cu")
 
 
 def _nvcc() -> str:
@@ -43,15 +45,25 @@ def needs_build(out: Path = LIB_PATH) -> bool:
 
 
 def build_library(force: bool = False, out: Path = LIB_PATH, extra_flags=()) -> Path:
-    """Compile csrc/moe_api.cu into ``out`` (default: the in-tree libmoe_b200.so)."""
+    """Compile the translation units (side by side) and link them into ``out`` (default: the
+    in-tree libmoe_b200.so)."""
     out = Path(out)
     if not force and not needs_build(out):
         return out
-    tmp = out.with_name(out.name + f".tmp{os.getpid()}")
-    cmd = [_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", str(INCLUDE), "-o", str(tmp),
-           str(CSRC / "moe_api.cu")]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, out)
+    tag = f".tmp{os.getpid()}"
+    tmp = out.with_name(out.name + tag)
+    objs = [out.with_name(u + tag + ".o") for u in UNITS]
+    common = [_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", str(INCLUDE)]
+    try:
+        procs = [subprocess.Popen([*common, "-c", "-o", str(o), str(CSRC / u)])
+                 for u, o in zip(UNITS, objs)]
+        if any([p.wait() != 0 for p in procs]):
+            raise RuntimeError("nvcc failed")
+        subprocess.run([*common, "-shared", "-o", str(tmp), *map(str, objs)], check=True)
+        os.replace(tmp, out)
+    finally:
+        for o in (*objs, tmp):
+            o.unlink(missing_ok=True)
     return out
 
 

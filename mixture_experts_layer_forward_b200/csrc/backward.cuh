@@ -199,6 +199,46 @@ __global__ void __launch_bounds__(BWD_THREADS)
     }
 }
 
+// Supplied routing: the gates' gradients dtopk_w[t][j] = dw of the pair's row, 0 for a pair that
+// was not dispatched (an id outside [0, E)).
+__global__ void __launch_bounds__(BWD_THREADS)
+    bwd_gates_kernel(const int32_t *__restrict__ inv_pos, const float *__restrict__ dw_row, int64_t n,
+                     int64_t rows, float *__restrict__ dtopk_w)
+{
+    const int64_t i = (int64_t)blockIdx.x * BWD_THREADS + threadIdx.x;
+    if (i >= n) return;
+    const int r = inv_pos[i];
+    dtopk_w[i] = (r >= 0 && r < rows) ? dw_row[r] : 0.0f;
+}
+
+// Supplied routing: dx[t] = sum_j dx_perm[inv_pos[t][j]] over the dispatched pairs, fp32 sum,
+// one bf16 rounding. One block per token (grid-stride), eight h per thread.
+__global__ void __launch_bounds__(BWD_THREADS)
+    bwd_dx_given_kernel(const __nv_bfloat16 *__restrict__ dx_perm, const int32_t *__restrict__ inv_pos,
+                        int64_t rows, int T, int H, int k, __nv_bfloat16 *__restrict__ dx)
+{
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        for (int i = threadIdx.x; i < H / 8; i += BWD_THREADS) {
+            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int j = 0; j < k; ++j) {
+                const int r = inv_pos[(size_t)t * k + j];
+                if (r < 0 || r >= rows) continue;
+                const uint4 v = reinterpret_cast<const uint4 *>(dx_perm + (size_t)r * H)[i];
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    acc[2 * q] += bwd_lo(vw[q]);
+                    acc[2 * q + 1] += bwd_hi(vw[q]);
+                }
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = bwd_pack(acc[2 * q], acc[2 * q + 1]);
+            reinterpret_cast<uint4 *>(dx + (size_t)t * H)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
 // dW_g[h][e] = sum over expert e's routed rows r of x[t_r][h] dl_r, and dbias[e] = sum dl_r
 // (with_bias == 0: the bias does not reach the gates, dbias = 0). Rows of expert e are
 // poff[e] .. poff[e] + counts[e] - 1 (routed rows first in each padded block), summed in

@@ -1,0 +1,621 @@
+// linear.cuh -- dense product with bias, activation and residual in its epilogue, on the
+// 5th-generation tensor cores, and the products of its gradient.
+//
+//   z = x W + bias,  y = act(z) + residual           (SwiGLU: z = [g, u], y = silu(g) u + r)
+//   dz = dy act'(z), dx = dz W^T, dW = x^T dz, dbias = sum over rows of dz
+//
+// All four products are one tile loop, D[m, n] = sum_k A[m, k] B[k, n], with each operand read
+// as it is stored: K-major (k contiguous) or MN-major (m or n contiguous).
+//   forward   A = x K-major;   B = W [K, N] MN-major, or W [N, K] K-major
+//   dx        A = dz K-major;  B = W^T: W [K, N] K-major, or W [N, K] MN-major
+//   dW        A and B MN-major: x^T dz [K, N], or dz^T x [N, K]
+// Edges need no padding: copies past a tensor's end read zeros, and the epilogue stores only
+// rows < M and columns < N.
+//
+// A block has ten warps: one issues TMA copies into a ring of 128-byte-swizzled stages (64
+// values of k each), one issues tcgen05.mma (M = 128, N = BN, fp32 accumulators in TMEM), eight
+// run the epilogue (each pair of warps shares 32 rows and splits the columns).
+//   linear_kernel        persistent, one block per SM, two accumulators, so that a tile's
+//                        epilogue runs beside the next tile's products.
+//   linear_split_kernel  one tile per cluster of S blocks, each with 1/S of k; the blocks'
+//                        accumulators meet through distributed shared memory, summed in rank
+//                        order (deterministic), and each block finishes 1/S of the columns.
+//                        For outputs of few tiles, where one block per tile would leave most
+//                        SMs idle: a token or a decode batch (bound by reading W), router
+//                        logits and weight gradients with few columns.
+// Every wait is bounded as in the other kernels here: a block that gives up records the
+// timeout, waits for its copies and products in flight, frees its TMEM and leaves.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace lin {
+constexpr int BM = 128;
+constexpr int BK = 64;
+constexpr int A_TILE = BM * BK * 2; // 16 KB
+constexpr int BOX = 64 * BK * 2;    // 8 KB: 64 columns x 64 k rows of an MN-major operand
+constexpr int THREADS = 320;        // TMA warp, MMA warp, 8 epilogue warps
+constexpr int EPI_THREADS = 256;
+__host__ __device__ constexpr int stage_bytes(int bn) { return A_TILE + bn * BK * 2; }
+__host__ __device__ constexpr int stages(int bn) { return 196608 / stage_bytes(bn); } // 4, 6, 8 for BN = 256, 128, 64
+__host__ __device__ constexpr int num_bars(int bn) { return 2 * stages(bn) + 5; }
+__host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages(bn) * stage_bytes(bn) + num_bars(bn) * 8 + 16; }
+} // namespace lin
+
+struct LinearArgs {
+    int M, N;             // output rows and columns
+    int m_tiles, n_tiles, k_blocks;
+    int group_m;          // m tiles that share a run of n tiles (operands of a run stay in L2)
+    int a_rows;           // rows of a K-major A box (M rounded up to 8, at most 128)
+    int act;              // 0 SwiGLU, 1 GELU (tanh form), 2 ReLU, 3 identity
+    int up_col;           // SwiGLU: first up column (= N); a tile holds BN/2 gate, BN/2 up columns
+    const float *bias;    // [N] ([2N] for SwiGLU) or nullptr
+    const __nv_bfloat16 *res; // [M, N], row stride ldr, or nullptr
+    int64_t ldr;
+    void *y;              // [M, N], row stride ldy
+    int64_t ldy;
+    int y_f32;
+    __nv_bfloat16 *z;     // pre-activation [M, N or 2N], row stride ldz, or nullptr
+    int64_t ldz;
+    int splits;           // linear_split_kernel: blocks per cluster
+    int *status;
+    int clear_status;     // block 0 clears the status word (the call's first launch with waits)
+    int64_t timeout_ns;
+};
+
+__device__ __forceinline__ void lin_bias8(const float *bias, float (&v)[8])
+{
+    const float4 a = reinterpret_cast<const float4 *>(bias)[0];
+    const float4 b = reinterpret_cast<const float4 *>(bias)[1];
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+}
+
+__device__ __forceinline__ uint4 lin_pack8(const float (&v)[8])
+{
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+// z * sigmoid(c z') forms with the fast exponential: its error reaches the product scaled by
+// the sigmoid, about 2^-22 of the value
+__device__ __forceinline__ float lin_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float lin_gelu(float z)
+{
+    const float c2 = 1.5957691216057308f; // 2 sqrt(2 / pi): (1 + tanh(w)) / 2 = 1 / (1 + exp(-2 w))
+    return __fdividef(z, 1.0f + __expf(-c2 * (z + 0.044715f * z * z * z)));
+}
+
+// Eight consecutive output columns of one row (col % 8 == 0, N % 8 == 0): v the accumulators
+// (SwiGLU: v the gate's, u the up's).
+__device__ __forceinline__ void lin_finish8(const LinearArgs &a, int row, int col, float (&v)[8],
+                                            float (&u)[8])
+{
+    if (row >= a.M || col >= a.N) return;
+    if (a.bias != nullptr) lin_bias8(a.bias + col, v);
+    if (a.act == 0) {
+        if (a.bias != nullptr) lin_bias8(a.bias + a.up_col + col, u);
+        if (a.z != nullptr) {
+            __nv_bfloat16 *zr = a.z + (size_t)row * a.ldz + col;
+            *reinterpret_cast<uint4 *>(zr) = lin_pack8(v);
+            *reinterpret_cast<uint4 *>(zr + a.up_col) = lin_pack8(u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = lin_silu(v[i]) * u[i];
+    } else {
+        if (a.z != nullptr)
+            *reinterpret_cast<uint4 *>(a.z + (size_t)row * a.ldz + col) = lin_pack8(v);
+        if (a.act == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = lin_gelu(v[i]);
+        } else if (a.act == 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+        }
+    }
+    if (a.res != nullptr) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(a.res + (size_t)row * a.ldr + col);
+        v[0] += bf16_lo(r.x); v[1] += bf16_hi(r.x); v[2] += bf16_lo(r.y); v[3] += bf16_hi(r.y);
+        v[4] += bf16_lo(r.z); v[5] += bf16_hi(r.z); v[6] += bf16_lo(r.w); v[7] += bf16_hi(r.w);
+    }
+    if (a.y_f32) {
+        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + (size_t)row * a.ldy + col);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + (size_t)row * a.ldy + col) =
+            lin_pack8(v);
+    }
+}
+
+__device__ __forceinline__ void lin_tile(int w, const LinearArgs &a, int &mt, int &nt)
+{
+    const int per = a.group_m * a.n_tiles;
+    const int g = w / per, r = w - g * per;
+    const int m0 = g * a.group_m;
+    const int gm = min(a.group_m, a.m_tiles - m0);
+    mt = m0 + r % gm;
+    nt = r / gm;
+}
+
+// The barriers and the two pipeline roles, shared by both kernels.
+template <int BN, bool A_MN, bool B_MN> struct LinPipe {
+    static constexpr int STAGES = lin::stages(BN);
+    static constexpr int STAGE = lin::stage_bytes(BN);
+    static constexpr uint32_t IDESC =
+        idesc_bf16_f32(lin::BM, BN, B_MN) | ((A_MN ? 1u : 0u) << 15);
+    uint8_t *smem;
+    uint32_t bar0;
+    int s = 0;       // ring position
+    uint32_t ph = 0;
+
+    __device__ uint32_t full(int i) const { return bar0 + 8u * i; }
+    __device__ uint32_t empty(int i) const { return bar0 + 8u * (STAGES + i); }
+    __device__ uint32_t tfull(int i) const { return bar0 + 8u * (2 * STAGES + i); }
+    __device__ uint32_t tempty(int i) const { return bar0 + 8u * (2 * STAGES + 2 + i); }
+    __device__ uint32_t done() const { return bar0 + 8u * (2 * STAGES + 4); }
+    __device__ void next()
+    {
+        if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+
+    // TMA copies of k-blocks [kb0, kb1) of one tile (one thread)
+    __device__ bool produce(const CUtensorMap &tmA, const CUtensorMap &tmB, const LinearArgs &a, int mt,
+                            int nt, int kb0, int kb1, volatile int *abort_flag, uint32_t &armed)
+    {
+        const bool gated = a.act == 0;
+        const int n0 = nt * (gated ? BN / 2 : BN);
+        const uint32_t bytes = (A_MN ? lin::A_TILE : a.a_rows * 128) + BN * 128;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_bounded(empty(s), ph ^ 1u, abort_flag, a.timeout_ns, a.status, 500)) return false;
+            const uint32_t a_dst = smem_u32(smem + s * STAGE), b_dst = a_dst + lin::A_TILE;
+            mbar_arrive_expect_tx(full(s), bytes);
+            armed |= 1u << s;
+            if (A_MN) {
+                tma_load_2d(a_dst, &tmA, full(s), mt * lin::BM, kb * lin::BK);
+                tma_load_2d(a_dst + lin::BOX, &tmA, full(s), mt * lin::BM + 64, kb * lin::BK);
+            } else {
+                tma_load_2d(a_dst, &tmA, full(s), kb * lin::BK, mt * lin::BM);
+            }
+            if (B_MN) {
+                constexpr int NB = BN / 64;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int col = (gated && i >= NB / 2) ? a.up_col + n0 + (i - NB / 2) * 64 : n0 + i * 64;
+                    tma_load_2d(b_dst + i * lin::BOX, &tmB, full(s), col, kb * lin::BK);
+                }
+            } else if (gated) { // box of BN / 2 rows
+                tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
+                tma_load_2d(b_dst + BN / 2 * 128, &tmB, full(s), kb * lin::BK, a.up_col + n0);
+            } else { // box of BN rows
+                tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
+            }
+            next();
+        }
+        return true;
+    }
+
+    // every copy issued has landed before the block leaves (ph, s: the next copy's place)
+    __device__ void drain(uint32_t armed, int64_t timeout_ns)
+    {
+        for (int i = 0; i < STAGES; ++i)
+            if ((armed >> i) & 1u) {
+                volatile int never = 0;
+                mbar_wait_bounded(full(i), i < s ? ph : ph ^ 1u, &never, timeout_ns, nullptr, 0);
+            }
+    }
+
+    // the products of k-blocks [kb0, kb1) into d_tmem (one thread)
+    __device__ bool multiply(const LinearArgs &a, uint32_t d_tmem, int kb0, int kb1,
+                             volatile int *abort_flag)
+    {
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_bounded(full(s), ph, abort_flag, a.timeout_ns, a.status, 510)) return false;
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(smem + s * STAGE), b_addr = a_addr + lin::A_TILE;
+            // K-major: rows of 128 bytes, +32 bytes per 16 k; MN-major: 64-column blocks of 64 k
+            // rows, +16 rows per 16 k
+            const uint64_t ad = A_MN ? sw128_desc(a_addr, lin::BOX, 1024) : sw128_desc(a_addr, 16, 1024);
+            const uint64_t bd = B_MN ? sw128_desc(b_addr, lin::BOX, 1024) : sw128_desc(b_addr, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < lin::BK / 16; ++k)
+                umma_bf16(d_tmem, ad + (uint64_t)((A_MN ? k * 2048 : k * 32) >> 4),
+                          bd + (uint64_t)((B_MN ? k * 2048 : k * 32) >> 4), IDESC,
+                          (kb != kb0 || k != 0) ? 1u : 0u);
+            umma_commit(empty(s));
+            next();
+        }
+        return true;
+    }
+};
+
+template <int BN, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(lin::THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ LinearArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    LinPipe<BN, A_MN, B_MN> p;
+    p.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~static_cast<uintptr_t>(1023));
+    constexpr int STAGES = lin::stages(BN);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + STAGES * lin::stage_bytes(BN));
+    p.bar0 = smem_u32(bars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        if (a.clear_status && blockIdx.x == 0) { // no wait can have run out yet
+            a.status[0] = DEV_OK;
+            a.status[1] = 0;
+        }
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(p.full(i), 1);
+            mbar_init(p.empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(p.tfull(i), 1);
+            mbar_init(p.tempty(i), 8);
+        }
+        mbar_init(p.done(), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 2 * BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = a.m_tiles * a.n_tiles;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t armed = 0;
+            for (int w = blockIdx.x; w < total; w += gridDim.x) {
+                int mt, nt;
+                lin_tile(w, a, mt, nt);
+                if (!p.produce(tmA, tmB, a, mt, nt, 0, a.k_blocks, abort_flag, armed)) break;
+            }
+            p.drain(armed, a.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            for (int w = blockIdx.x; w < total; w += gridDim.x, ++it) {
+                const int acc = it & 1;
+                if (!mbar_wait_bounded(p.tempty(acc), ((it >> 1) & 1) ^ 1, abort_flag, a.timeout_ns,
+                                       a.status, 520))
+                    break;
+                tc_fence_after();
+                if (!p.multiply(a, tmem + acc * BN, 0, a.k_blocks, abort_flag)) break;
+                umma_commit(p.tfull(acc));
+            }
+            umma_commit(p.done()); // every product is finished before TMEM is released
+            volatile int never = 0;
+            mbar_wait_bounded(p.done(), 0, &never, a.timeout_ns, a.status, 530);
+        }
+    } else {
+        const int q = warp & 3, half = warp >= 6 ? 1 : 0;
+        const bool gated = a.act == 0;
+        const int tc = gated ? BN / 2 : BN;
+        const int chunks = tc / 32;
+        const int c0 = half * ((chunks + 1) / 2), c1 = half ? chunks : (chunks + 1) / 2;
+        int it = 0;
+        for (int w = blockIdx.x; w < total; w += gridDim.x, ++it) {
+            int mt, nt;
+            lin_tile(w, a, mt, nt);
+            const int acc = it & 1;
+            const bool ok = mbar_wait_bounded(p.tfull(acc), (it >> 1) & 1, abort_flag, a.timeout_ns,
+                                              a.status, 540);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+            const int row = mt * lin::BM + q * 32 + lane;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                if (nt * tc + c * 32 >= a.N) break;
+                uint32_t r[32], u[32];
+                tmem_ld_32x32b_x32(t_row + c * 32, r);
+                if (gated) tmem_ld_32x32b_x32(t_row + BN / 2 + c * 32, u);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v[8], x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[j] = __uint_as_float(r[i * 8 + j]);
+                        x[j] = gated ? __uint_as_float(u[i * 8 + j]) : 0.0f;
+                    }
+                    lin_finish8(a, row, nt * tc + c * 32 + i * 8, v, x);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p.tempty(acc));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// One tile per cluster of a.splits blocks (launched with that cluster width).
+template <int BN, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(lin::THREADS, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ LinearArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    LinPipe<BN, A_MN, B_MN> p;
+    p.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~static_cast<uintptr_t>(1023));
+    constexpr int STAGES = lin::stages(BN);
+    constexpr int LD = BN + 4; // fp32 row of the parked accumulators: 16-byte writes of 8 rows meet no bank twice
+    static_assert(lin::BM * LD * 4 <= STAGES * lin::stage_bytes(BN), "the parked tile fits the stages");
+    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + STAGES * lin::stage_bytes(BN));
+    p.bar0 = smem_u32(bars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = a.splits;
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    if (threadIdx.x == 0) {
+        if (a.clear_status && blockIdx.x == 0) {
+            a.status[0] = DEV_OK;
+            a.status[1] = 0;
+        }
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(p.full(i), 1);
+            mbar_init(p.empty(i), 1);
+        }
+        mbar_init(p.tfull(0), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    int mt, nt;
+    lin_tile(blockIdx.x / S, a, mt, nt);
+    const int kb0 = (int)((int64_t)rank * a.k_blocks / S), kb1 = (int)((int64_t)(rank + 1) * a.k_blocks / S);
+    const bool gated = a.act == 0;
+    const int tc = gated ? BN / 2 : BN;
+    const int rows = min(lin::BM, a.M - mt * lin::BM);
+    float *park = reinterpret_cast<float *>(p.smem);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t armed = 0;
+            p.produce(tmA, tmB, a, mt, nt, kb0, kb1, abort_flag, armed);
+            p.drain(armed, a.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            p.multiply(a, tmem, kb0, kb1, abort_flag);
+            umma_commit(p.tfull(0)); // every product issued is finished
+        }
+    } else {
+        const int q = warp & 3, half = warp >= 6 ? 1 : 0;
+        // the products issued finish on their own: this wait ends with them, or runs out
+        volatile int never = 0;
+        const bool ok = mbar_wait_bounded(p.tfull(0), 0, &never, 2 * a.timeout_ns, a.status, 540);
+        if (__all_sync(0xffffffffu, ok) && q * 32 < rows) {
+            tc_fence_after();
+            const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
+            float *dst = park + (q * 32 + lane) * LD;
+#pragma unroll 1
+            for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(t_row + c * 32, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(dst + c * 32 + i * 4) =
+                        make_uint4(r[i * 4], r[i * 4 + 1], r[i * 4 + 2], r[i * 4 + 3]);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (S > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, BN);
+    }
+    if (warp >= 2) {
+        // this block's 1/S of the tile's columns, eight at a time
+        const int vec = tc / 8;
+        const int v0 = rank * vec / S, nv = (rank + 1) * vec / S - v0;
+        const uint32_t base = smem_u32(park);
+        uint32_t peer[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) peer[s] = (S > 1 && s < S) ? mapa_shared(base, (uint32_t)s) : base;
+        for (int i = threadIdx.x - 64; i < rows * nv; i += lin::EPI_THREADS) {
+            const int row = i / nv, c = (v0 + i - row * nv) * 8;
+            if (nt * tc + c >= a.N) continue;
+            const uint32_t off = (uint32_t)(row * LD + c) * 4u;
+            float v[8], u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                if (s < S) {
+                    const float4 x0 = ld_cluster_f4(peer[s] + off), x1 = ld_cluster_f4(peer[s] + off + 16);
+                    v[0] += x0.x; v[1] += x0.y; v[2] += x0.z; v[3] += x0.w;
+                    v[4] += x1.x; v[5] += x1.y; v[6] += x1.z; v[7] += x1.w;
+                    if (gated) {
+                        const float4 y0 = ld_cluster_f4(peer[s] + off + BN * 2);
+                        const float4 y1 = ld_cluster_f4(peer[s] + off + BN * 2 + 16);
+                        u[0] += y0.x; u[1] += y0.y; u[2] += y0.z; u[3] += y0.w;
+                        u[4] += y1.x; u[5] += y1.y; u[6] += y1.z; u[7] += y1.w;
+                    }
+                }
+            }
+            lin_finish8(a, mt * lin::BM + row, nt * tc + c, v, u);
+        }
+    }
+    if (S > 1) {
+        __syncwarp();
+        cluster_sync_all(); // no block leaves while a peer may still read its accumulators
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// the gradient at the pre-activation
+// ---------------------------------------------------------------------------------------
+
+struct LinearDzArgs {
+    const void *dy; // [M, N] bf16 or fp32, row stride ldy
+    int64_t ldy;
+    int dy_f32;
+    const __nv_bfloat16 *z; // [M, N or 2N], row stride ldz (identity: not read)
+    int64_t ldz;
+    __nv_bfloat16 *dz;      // [M, N or 2N] dense, or nullptr (only the column sums are wanted)
+    float *part;            // [chunks, N or 2N] column sums of each row chunk, or nullptr
+    int M, N, act;
+    int rows;               // rows per chunk
+};
+
+__device__ __forceinline__ float lin_gelu_grad(float z)
+{
+    const float c2 = 1.5957691216057308f;
+    const float s = __fdividef(1.0f, 1.0f + __expf(-c2 * (z + 0.044715f * z * z * z)));
+    return s + z * s * (1.0f - s) * c2 * (1.0f + 3.0f * 0.044715f * z * z);
+}
+
+// dz (bf16, the products' operand) and the column sums of the unrounded dz, in one pass over dy
+// and z. A block has 32 x 8 threads: 32 vectors of eight columns, eight rows at a time; the
+// sums over a chunk's rows run in fp32 in a fixed order (rows of one thread, then the eight
+// threads). Bound by the bytes of dy, z and dz.
+__global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ LinearDzArgs a)
+{
+    __shared__ float red[8][32][17];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int col = (blockIdx.x * 32 + tx) * 8;
+    const bool gated = a.act == 0;
+    const int cols = gated ? 2 * a.N : a.N;
+    const int r1 = min(a.M, ((int)blockIdx.y + 1) * a.rows);
+    float sg[8], su[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+    if (col < a.N) {
+        for (int row = blockIdx.y * a.rows + ty; row < r1; row += 8) {
+            float d[8], g[8], u[8];
+            if (a.dy_f32) {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.dy) +
+                                                                   (size_t)row * a.ldy + col);
+                const float4 x = p[0], y = p[1];
+                d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+                d[4] = y.x; d[5] = y.y; d[6] = y.z; d[7] = y.w;
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(a.dy) + (size_t)row * a.ldy + col);
+                d[0] = bf16_lo(x.x); d[1] = bf16_hi(x.x); d[2] = bf16_lo(x.y); d[3] = bf16_hi(x.y);
+                d[4] = bf16_lo(x.z); d[5] = bf16_hi(x.z); d[6] = bf16_lo(x.w); d[7] = bf16_hi(x.w);
+            }
+            if (a.act != 3) {
+                const __nv_bfloat16 *zr = a.z + (size_t)row * a.ldz + col;
+                const uint4 x = *reinterpret_cast<const uint4 *>(zr);
+                g[0] = bf16_lo(x.x); g[1] = bf16_hi(x.x); g[2] = bf16_lo(x.y); g[3] = bf16_hi(x.y);
+                g[4] = bf16_lo(x.z); g[5] = bf16_hi(x.z); g[6] = bf16_lo(x.w); g[7] = bf16_hi(x.w);
+                if (gated) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(zr + a.N);
+                    u[0] = bf16_lo(y.x); u[1] = bf16_hi(y.x); u[2] = bf16_lo(y.y); u[3] = bf16_hi(y.y);
+                    u[4] = bf16_lo(y.z); u[5] = bf16_hi(y.z); u[6] = bf16_lo(y.w); u[7] = bf16_hi(y.w);
+                }
+            }
+            if (gated) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float s = __fdividef(1.0f, 1.0f + __expf(-g[i]));
+                    const float dg = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+                    const float du = d[i] * g[i] * s;
+                    d[i] = dg;
+                    u[i] = du;
+                    sg[i] += dg;
+                    su[i] += du;
+                }
+                if (a.dz != nullptr) {
+                    __nv_bfloat16 *o = a.dz + (size_t)row * cols + col;
+                    *reinterpret_cast<uint4 *>(o) = lin_pack8(d);
+                    *reinterpret_cast<uint4 *>(o + a.N) = lin_pack8(u);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (a.act == 1) d[i] *= lin_gelu_grad(g[i]);
+                    if (a.act == 2) d[i] = g[i] > 0.0f ? d[i] : 0.0f;
+                    sg[i] += d[i];
+                }
+                if (a.dz != nullptr)
+                    *reinterpret_cast<uint4 *>(a.dz + (size_t)row * cols + col) = lin_pack8(d);
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        red[ty][tx][i] = sg[i];
+        red[ty][tx][8 + i] = su[i];
+    }
+    __syncthreads();
+    // 256 gate (or plain) sums, then 256 up sums
+    for (int h = 0; h < (gated ? 2 : 1); ++h) {
+        const int v = threadIdx.x >> 3, i = threadIdx.x & 7;
+        const int c = (blockIdx.x * 32 + v) * 8 + i;
+        if (c < a.N) {
+            float s = 0.0f;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) s += red[y][v][h * 8 + i];
+            a.part[(size_t)blockIdx.y * cols + h * a.N + c] = s;
+        }
+    }
+}
+
+// dbias[c] = the chunks' sums, in chunk order.
+__global__ void __launch_bounds__(256)
+    linear_dbias_kernel(const float *__restrict__ part, int chunks, int cols, float *__restrict__ dbias)
+{
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < chunks; ++i) s += part[(size_t)i * cols + c];
+    dbias[c] = s;
+}
+
+} // namespace moe

@@ -17,6 +17,7 @@
 #include "ep.cuh"
 #include "fp8.cuh"
 #include "fused.cuh"
+#include "host.cuh"
 #include "route_chain.cuh"
 #include "gemm_tc.cuh"
 #include "ptx.cuh"
@@ -24,12 +25,15 @@
 #include "route_filter.cuh"
 #include "gemm_narrow.cuh"
 
+namespace moe {
+constexpr int64_t kDefaultTimeoutNs = 2000000000LL;
+std::atomic<int64_t> g_timeout_ns{kDefaultTimeoutNs};
+} // namespace moe
+
 namespace {
 
 using namespace moe;
 
-constexpr int64_t kDefaultTimeoutNs = 2000000000LL;
-std::atomic<int64_t> g_timeout_ns{kDefaultTimeoutNs};
 // grouped GEMM variant: MOE_GEMM_AUTO / MOE_GEMM_SINGLE_CTA / MOE_GEMM_CTA_PAIR
 std::atomic<int> g_gemm_mode{MOE_GEMM_AUTO};
 // test hook: layer0 work item of the fused kernel whose ready signal is withheld (-1: none)
@@ -230,47 +234,6 @@ template <typename T> T *at(void *ws, size_t off)
 
 struct FilterBufs;
 FilterBufs filter_bufs(void *ws, const Layout &L);
-
-bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-bool aligned4(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
-
-// ---------------------------------------------------------------------------------------
-// device properties and tensor maps
-// ---------------------------------------------------------------------------------------
-
-int sm_count()
-{
-    static std::atomic<int> cache[64]; // per device; 0 = not yet queried (static: zeroed)
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev < 0 || dev >= 64) return 0;
-    int n = cache[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cache[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    });
-    return fn;
-}
 
 // 2D bf16 row-major [rows, cols]; box = 64 columns x box_rows rows, 128-byte swizzle.
 bool make_map_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows)
@@ -834,8 +797,6 @@ FrontPlan front_plan(const moe_problem *p)
     return f;
 }
 
-moe_status to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
 // Fixed logits scratch of moe_route_noalloc: one copy per GPU that loads the library, held
 // until the process exits. Only device code may name it directly; host code must use the
 // address that cudaGetSymbolAddress returns for the current device.
@@ -1242,6 +1203,18 @@ moe_status forward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16 
     return to_status(e);
 }
 
+moe_status check_shared(const moe_problem *p, const moe_shared_expert *shared, size_t ws_bytes)
+{
+    if (shared == nullptr || shared->F_s <= 0 || shared->W1s == nullptr || shared->W2s == nullptr)
+        return MOE_ERR_INVALID_ARG;
+    if (shared->F_s % 64 != 0) return MOE_ERR_UNSUPPORTED;
+    if (!aligned16(shared->W1s) || !aligned16(shared->W2s) ||
+        (shared->w_sg != nullptr && !aligned16(shared->w_sg)))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < make_layout(p, shared->F_s).end_shared) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
 template <int BMODE>
 cudaError_t launch_gemm_bwd(const CUtensorMap &ta, const CUtensorMap &tb, const GemmArgs &args,
                             int max_work, cudaStream_t st)
@@ -1277,19 +1250,24 @@ moe_status check_problem_bwd(const moe_problem *p)
 moe_status backward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16 *Wg,
                          const float *bias, const moe_bf16 *W1, const moe_bf16 *W2,
                          const moe_bf16 *dy, moe_bf16 *dx, float *dWg, float *dbias, moe_bf16 *dW1,
-                         moe_bf16 *dW2, void *ws, size_t ws_bytes, cudaStream_t st)
+                         moe_bf16 *dW2, void *ws, size_t ws_bytes, cudaStream_t st,
+                         const int32_t *given_idx = nullptr, const float *given_w = nullptr,
+                         float *dtopk_w = nullptr, bool given = false)
 {
     moe_status s = check_problem_bwd(p);
     if (s != MOE_OK) return s;
-    if (ws == nullptr || Wg == nullptr || W1 == nullptr || W2 == nullptr || dWg == nullptr ||
-        dbias == nullptr || dW1 == nullptr || dW2 == nullptr ||
-        (p->T > 0 && (x == nullptr || dy == nullptr || dx == nullptr)))
+    // given: the routing is supplied; no router gradients, the gates' own in dtopk_w
+    if (ws == nullptr || W1 == nullptr || W2 == nullptr || dW1 == nullptr || dW2 == nullptr ||
+        (!given && (Wg == nullptr || dWg == nullptr || dbias == nullptr)) ||
+        (p->T > 0 && (x == nullptr || dy == nullptr || dx == nullptr)) ||
+        (given && p->T > 0 && (given_idx == nullptr || given_w == nullptr || dtopk_w == nullptr)))
         return MOE_ERR_INVALID_ARG;
     const Layout L = make_layout(p, 0, false, true);
     if (ws_bytes < L.end_bwd) return MOE_ERR_WORKSPACE;
     if (!aligned16(x) || !aligned16(Wg) || !aligned16(W1) || !aligned16(W2) || !aligned16(dy) ||
         !aligned16(dx) || !aligned16(dW1) || !aligned16(dW2) || !aligned4(dWg) || !aligned4(dbias) ||
-        !aligned4(bias) || !aligned16(ws))
+        !aligned4(bias) || !aligned16(ws) || !aligned4(given_idx) || !aligned4(given_w) ||
+        !aligned4(dtopk_w))
         return MOE_ERR_INVALID_ARG;
     const int T = p->T, H = p->H, F = p->F, E = p->E, k = p->top_k;
     const bool gated = (p->act == MOE_ACT_SWIGLU);
@@ -1297,14 +1275,14 @@ moe_status backward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16
     int *status = at<int>(ws, L.status);
     if (T == 0) { // no rows: every gradient is zero
         cudaError_t e = cudaMemsetAsync(status, 0, 8, st);
-        if (e == cudaSuccess) e = cudaMemsetAsync(dWg, 0, (size_t)H * E * 4, st);
-        if (e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, (size_t)E * 4, st);
+        if (e == cudaSuccess && !given) e = cudaMemsetAsync(dWg, 0, (size_t)H * E * 4, st);
+        if (e == cudaSuccess && !given) e = cudaMemsetAsync(dbias, 0, (size_t)E * 4, st);
         if (e == cudaSuccess) e = cudaMemsetAsync(dW1, 0, (size_t)E * H * w1c * 2, st);
         if (e == cudaSuccess) e = cudaMemsetAsync(dW2, 0, (size_t)E * F * H * 2, st);
         return to_status(e);
     }
-    int32_t *topk_idx = at<int32_t>(ws, L.topk_idx);
-    float *topk_w = at<float>(ws, L.topk_w);
+    const int32_t *topk_idx = given ? given_idx : at<int32_t>(ws, L.topk_idx);
+    const float *topk_w = given ? given_w : at<float>(ws, L.topk_w);
     DispatchOut d = dispatch_bufs(ws, L);
     d.active_list = at<int32_t>(ws, L.bact);
     moe_bf16 *x_perm = at<moe_bf16>(ws, L.x_perm);
@@ -1328,9 +1306,12 @@ moe_status backward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16
         return MOE_ERR_CUDA;
     const int64_t timeout = g_timeout_ns.load();
     const FilterBufs fb = filter_bufs(ws, L);
-    cudaError_t e = launch_route(p, x, Wg, bias, topk_idx, topk_w, at<float>(ws, L.logits), status,
-                                 st, &fb);
-    if (e == cudaSuccess) e = launch_dispatch(p, L, topk_idx, topk_w, d, status, 0, st);
+    cudaError_t e = cudaSuccess;
+    if (!given)
+        e = launch_route(p, x, Wg, bias, at<int32_t>(ws, L.topk_idx), at<float>(ws, L.topk_w),
+                         at<float>(ws, L.logits), status, st, &fb);
+    // with the routing supplied the dispatch clears the status word (and checks the ids)
+    if (e == cudaSuccess) e = launch_dispatch(p, L, topk_idx, topk_w, d, status, given ? 1 : 0, st);
     if (e == cudaSuccess) e = launch_gather(p, x, d.gather_idx, d.meta, x_perm, st);
 
     GemmArgs g{};
@@ -1374,8 +1355,13 @@ moe_status backward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16
             dw_row);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && !given) {
         bwd_router_kernel<<<(T * 32 + 255) / 256, 256, 0, st>>>(topk_w, d.inv_pos, dw_row, T, k, dl_row);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && given) {
+        const int64_t n = (int64_t)T * k;
+        bwd_gates_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(d.inv_pos, dw_row, n, L.pmax, dtopk_w);
         e = cudaGetLastError();
     }
     // weight gradients: zero for the experts without rows; dW2[e] = a_e^T gy_e and
@@ -1418,13 +1404,18 @@ moe_status backward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16
         int grid = sm_count() * 8;
         if (grid <= 0) grid = 1184;
         if (grid > T) grid = T;
-        bwd_dx_kernel<<<grid, BWD_THREADS, 0, st>>>(reinterpret_cast<const __nv_bfloat16 *>(dxp),
-                                                     d.inv_pos, topk_idx, dl_row,
-                                                     reinterpret_cast<const __nv_bfloat16 *>(Wg), T,
-                                                     H, E, k, reinterpret_cast<__nv_bfloat16 *>(dx));
+        if (given)
+            bwd_dx_given_kernel<<<grid, BWD_THREADS, 0, st>>>(
+                reinterpret_cast<const __nv_bfloat16 *>(dxp), d.inv_pos, L.pmax, T, H, k,
+                reinterpret_cast<__nv_bfloat16 *>(dx));
+        else
+            bwd_dx_kernel<<<grid, BWD_THREADS, 0, st>>>(
+                reinterpret_cast<const __nv_bfloat16 *>(dxp), d.inv_pos, topk_idx, dl_row,
+                reinterpret_cast<const __nv_bfloat16 *>(Wg), T, H, E, k,
+                reinterpret_cast<__nv_bfloat16 *>(dx));
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && !given) {
         bwd_router_weights_kernel<<<dim3(E, (H + BWD_THREADS - 1) / BWD_THREADS), BWD_THREADS, 0, st>>>(
             reinterpret_cast<const __nv_bfloat16 *>(x), d.gather_idx, d.poff, d.counts, dl_row, H, E,
             (bias != nullptr && p->gate != MOE_GATE_SELECT_BIAS) ? 1 : 0, dWg, dbias);
@@ -2046,13 +2037,8 @@ moe_status moe_forward_shared(const moe_problem *p, const moe_bf16 *x, const moe
 {
     moe_status s = check_problem(p);
     if (s != MOE_OK) return s;
-    if (shared == nullptr || shared->F_s <= 0 || shared->W1s == nullptr || shared->W2s == nullptr)
-        return MOE_ERR_INVALID_ARG;
-    if (shared->F_s % 64 != 0) return MOE_ERR_UNSUPPORTED;
-    if (!aligned16(shared->W1s) || !aligned16(shared->W2s) ||
-        (shared->w_sg != nullptr && !aligned16(shared->w_sg)))
-        return MOE_ERR_INVALID_ARG;
-    if (ws_bytes < make_layout(p, shared->F_s).end_shared) return MOE_ERR_WORKSPACE;
+    const moe_status c = check_shared(p, shared, ws_bytes);
+    if (c != MOE_OK) return c;
     return forward_impl(p, x, Wg, bias, W1, W2, out, topk_idx_out, topk_w_out, ws, ws_bytes,
                         static_cast<cudaStream_t>(stream), nullptr, 0, shared);
 }
@@ -2263,6 +2249,35 @@ moe_status moe_experts_forward(const moe_problem *p, const moe_bf16 *x, const in
     return forward_impl(p, x, nullptr, nullptr, W1, W2, out, nullptr, nullptr, ws, ws_bytes,
                         static_cast<cudaStream_t>(stream), nullptr, 0, nullptr,
                         p != nullptr && p->T > 0 ? expert : nullptr, gate);
+}
+
+moe_status moe_forward_routed(const moe_problem *p, const moe_bf16 *x, const int32_t *topk_idx,
+                              const float *topk_w, const moe_bf16 *W1, const moe_bf16 *W2,
+                              const moe_shared_expert *shared, moe_bf16 *out, void *ws, size_t ws_bytes,
+                              void *stream)
+{
+    const moe_status s = check_problem(p);
+    if (s != MOE_OK) return s;
+    if (p->T > 0 && (topk_idx == nullptr || topk_w == nullptr || !aligned4(topk_idx) || !aligned4(topk_w)))
+        return MOE_ERR_INVALID_ARG;
+    if (shared != nullptr) {
+        const moe_status c = check_shared(p, shared, ws_bytes);
+        if (c != MOE_OK) return c;
+    }
+    // T == 0 launches nothing; any non-null pointer marks the routing as supplied
+    static const int32_t none = 0;
+    return forward_impl(p, x, nullptr, nullptr, W1, W2, out, nullptr, nullptr, ws, ws_bytes,
+                        static_cast<cudaStream_t>(stream), nullptr, 0, shared,
+                        p->T > 0 ? topk_idx : &none, topk_w);
+}
+
+moe_status moe_backward_routed(const moe_problem *p, const moe_bf16 *x, const int32_t *topk_idx,
+                               const float *topk_w, const moe_bf16 *W1, const moe_bf16 *W2,
+                               const moe_bf16 *dout, moe_bf16 *dx, float *dtopk_w, moe_bf16 *dW1,
+                               moe_bf16 *dW2, void *ws, size_t ws_bytes, void *stream)
+{
+    return backward_impl(p, x, nullptr, nullptr, W1, W2, dout, dx, nullptr, nullptr, dW1, dW2, ws,
+                         ws_bytes, static_cast<cudaStream_t>(stream), topk_idx, topk_w, dtopk_w, true);
 }
 
 moe_status moe_experts_forward_n(const moe_problem *p, const moe_bf16 *x, const int32_t *expert,
