@@ -42,24 +42,30 @@ moe_status check_select(const moe_select *s)
 int dtype_bytes(int32_t d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 bool aligned_to(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % (unsigned)bytes) == 0; }
 
-template <int EPT, typename LT>
+template <int EPT, typename LT, bool BIASED>
 cudaError_t launch_select(const SelectArgs &a, cudaStream_t st)
 {
-    // four tokens per block above 512 experts, so that the scratch stays within 48 KB
-    const int warps = a.E > 512 ? 4 : 8;
-    const size_t smem = (size_t)warps * a.E * sizeof(unsigned long long);
-    route_select_kernel<EPT, LT><<<(unsigned)((a.T + warps - 1) / warps), warps * 32, smem, st>>>(a);
+    constexpr int warps = sel_threads(EPT) / 32; // the scratch stays within 48 KB
+    const size_t smem = (size_t)warps * (a.E + 34) * sizeof(unsigned long long);
+    const int sms = sm_count() > 0 ? sm_count() : 148;
+    const unsigned grid = (unsigned)std::min((a.T + warps - 1) / warps, sms * sel_blocks(EPT));
+    route_select_kernel<EPT, LT, BIASED><<<grid, warps * 32, smem, st>>>(a);
     return cudaGetLastError();
+}
+
+template <typename LT, bool BIASED> cudaError_t launch_select_wide(const SelectArgs &a, cudaStream_t st)
+{
+    if (a.E <= 32) return launch_select<1, LT, BIASED>(a, st);
+    if (a.E <= 64) return launch_select<2, LT, BIASED>(a, st);
+    if (a.E <= 128) return launch_select<4, LT, BIASED>(a, st);
+    if (a.E <= 256) return launch_select<8, LT, BIASED>(a, st);
+    if (a.E <= 512) return launch_select<16, LT, BIASED>(a, st);
+    return launch_select<32, LT, BIASED>(a, st);
 }
 
 template <typename LT> cudaError_t launch_select_any(const SelectArgs &a, cudaStream_t st)
 {
-    if (a.E <= 32) return launch_select<1, LT>(a, st);
-    if (a.E <= 64) return launch_select<2, LT>(a, st);
-    if (a.E <= 128) return launch_select<4, LT>(a, st);
-    if (a.E <= 256) return launch_select<8, LT>(a, st);
-    if (a.E <= 512) return launch_select<16, LT>(a, st);
-    return launch_select<32, LT>(a, st);
+    return a.bias != nullptr ? launch_select_wide<LT, true>(a, st) : launch_select_wide<LT, false>(a, st);
 }
 
 // ---------------------------------------------------------------------------------------

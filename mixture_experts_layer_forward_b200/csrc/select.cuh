@@ -14,13 +14,21 @@
 // The selection is the one that keys in 64 bits give. Keys are first formed in 32 bits with the
 // fast exponential, whose distance from the 64-bit key is bounded (SEL_TOL_*). Where every
 // decision of a token was clear of that bound the 32-bit selection is the 64-bit one; otherwise
-// the warp forms the token's keys again in 64 bits (sel_exact). Without a bias, and without
-// sums over groups, the keys are the logits themselves and no bound is needed.
+// (about 1 token in 1000 of random logits; ties) the warp selects again with 64-bit keys
+// (sel_exact).
 //
-// One warp per token; lane i owns the EPT consecutive experts from i * EPT, so the lowest lane
-// with the largest key holds the lowest expert id. k rounds: the lanes' own maxima (as
-// order-preserving unsigned integers) meet in one redux.sync, the first lane that holds it
-// gives up that expert. The weights are computed once for all k on the first k lanes.
+// One warp per token, tokens in a grid-stride loop with the next row's logits in flight; lane i
+// owns the EPT consecutive experts from i * EPT. With 256 experts a row is 1 KB and the work is
+// some 400 warp instructions, so the kernel is bound by instructions, not bytes, and is built to
+// spend few per key:
+//   - a key carries its place in the lane in its lowest log2(EPT) mantissa bits (counted in the
+//     bound), so a key and its expert sort as one float: min and max, nothing else;
+//   - each lane sorts its keys once (19 exchanges for 8); a round of the top-k is then one
+//     redux.sync over the lanes' heads, and the winning lane drops its head;
+//   - a group's two largest keys are the heads of its lanes;
+//   - the checks against the bound are made once, after the rounds, on the k winners' lanes.
+// bf16 logits without a bias leave 16 mantissa bits free: the key carries the whole expert id and the
+// 32-bit order is exact, ties included.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,10 +45,16 @@ constexpr int SEL_MAX_GROUPS = 32; // one group per lane
 //   1 + e adds 2^-24 s, the quotient 2 ulp: 3.8e-7 a key, 7.6e-7 for two;
 // softmax: 3.2e-7 s_max a key from the exponential, and one factor common to all keys (the sum:
 //   36 rounded additions and the terms' own errors, the reciprocal) of at most 4.1e-6: 4.8e-6;
-// the sum with the bias rounds by 2^-24 of the key.
+// the sum with the bias rounds by 2^-24 of the key, the place by at most EPT 2^-23 of it.
 constexpr float SEL_TOL_SIGMOID = 9.5367431640625e-7f; // 2^-20
 constexpr float SEL_TOL_SOFTMAX = 7.62939453125e-6f;   // 2^-17, times the largest score
 constexpr float SEL_TOL_KEY = 2.384185791015625e-7f;   // 2^-22, times the key
+constexpr float SEL_TOL_ZERO = 1.0e-40f;               // a place in a zero or denormal key
+__host__ __device__ constexpr float SEL_PLACE(int ept) { return ept * 1.1920928955078125e-7f; } // EPT 2^-23
+// Masked or excluded experts' key, and the clamp of the others; a winner at or beyond SEL_EDGE
+// (also a lane whose sorted keys ran out) sends the token to sel_exact.
+constexpr float SEL_FAR = 3.0e38f;
+constexpr float SEL_EDGE = 2.9e38f;
 
 struct SelectArgs {
     const void *logits; // [T, E], row stride ld (elements)
@@ -66,30 +80,27 @@ __device__ __forceinline__ float sel_clean(float l)
     return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
 }
 
-// Order-preserving integers of keys. 0 is no candidate, 1 a masked expert; a NaN key (a NaN
-// bias) counts as -inf.
-__device__ __forceinline__ uint32_t sel_ord(float key)
-{
-    if (key != key) key = -INFINITY;
-    const uint32_t u = __float_as_uint(key + 0.0f); // -0 and +0 are equal keys
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float sel_unord(uint32_t o)
-{
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
-}
+// Order-preserving integers of 64-bit keys: 0 is no candidate, 1 a masked expert; a NaN key (a
+// NaN bias) counts as -inf.
 __device__ __forceinline__ unsigned long long sel_ord64(double key)
 {
     if (key != key) key = -INFINITY;
     const unsigned long long u = (unsigned long long)__double_as_longlong(key + 0.0);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
-constexpr uint32_t SEL_MASKED = 1u;
-constexpr uint32_t SEL_NEG_INF = 0x007fffffu; // sel_ord(-inf)
+constexpr unsigned long long SEL_MASKED = 1ull;
 
 __device__ __forceinline__ float sel_max(float v)
 {
-    return sel_unord(__reduce_max_sync(0xffffffffu, sel_ord(v)));
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float sel_min(float v)
+{
+    float r;
+    asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 __device__ __forceinline__ float sel_sum(float v)
 {
@@ -111,11 +122,15 @@ __device__ __forceinline__ bool sel_group_stays(V gv, int groups, int keep, int 
     return lane < groups && rank < keep;
 }
 
+struct SelExact {
+    int mine;     // the expert selected in round `lane` (lane < k)
+    float m, sum; // softmax: the row's maximum and sum
+};
+
 // The selection with keys in 64 bits. key: E order words of this warp in shared memory.
-// Returns the expert selected in round `lane` (lane < k).
 template <typename LT>
-__device__ __noinline__ int sel_exact(const SelectArgs &a, const LT *row, unsigned long long *key,
-                                      int lane)
+__device__ __noinline__ SelExact sel_exact(const SelectArgs &a, const LT *row, unsigned long long *key,
+                                           int lane)
 {
     double m = -INFINITY, sum = 0.0;
     if (!a.sigmoid) {
@@ -187,23 +202,50 @@ __device__ __noinline__ int sel_exact(const SelectArgs &a, const LT *row, unsign
         if (lane == 0) key[be] = 0;
         __syncwarp();
     }
-    return mine;
+    return SelExact{mine, (float)m, sum > 0.0 ? (float)sum : 1.0f};
 }
 
-// Dynamic shared memory: per warp E order words (sel_exact; the group values' scratch).
-template <int EPT, typename LT>
-__global__ void __launch_bounds__(256) route_select_kernel(const __grid_constant__ SelectArgs a)
+// Descending order of n keys (n = 2, 4, 8), by compare-exchange of minimum and maximum.
+__device__ __forceinline__ void sel_cx(float &a, float &b)
 {
-    extern __shared__ unsigned long long sel_smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * (blockDim.x >> 5) + warp;
-    if (t >= a.T || (a.n_rows != nullptr && t >= *a.n_rows)) return;
-    const LT *row = static_cast<const LT *>(a.logits) + (size_t)t * a.ld;
-    unsigned long long *scratch = sel_smem + (size_t)warp * a.E;
-    const int e0 = lane * EPT;
-    constexpr int PV = 16 / (int)sizeof(LT); // values in 16 bytes
+    const float hi = fmaxf(a, b);
+    b = fminf(a, b);
+    a = hi;
+}
+template <int N> __device__ __forceinline__ void sel_sort(float *v)
+{
+    if constexpr (N == 2) {
+        sel_cx(v[0], v[1]);
+    } else if constexpr (N == 4) {
+        sel_cx(v[0], v[2]); sel_cx(v[1], v[3]);
+        sel_cx(v[0], v[1]); sel_cx(v[2], v[3]);
+        sel_cx(v[1], v[2]);
+    } else if constexpr (N == 8) {
+        sel_cx(v[0], v[2]); sel_cx(v[1], v[3]); sel_cx(v[4], v[6]); sel_cx(v[5], v[7]);
+        sel_cx(v[0], v[4]); sel_cx(v[1], v[5]); sel_cx(v[2], v[6]); sel_cx(v[3], v[7]);
+        sel_cx(v[0], v[1]); sel_cx(v[2], v[3]); sel_cx(v[4], v[5]); sel_cx(v[6], v[7]);
+        sel_cx(v[2], v[4]); sel_cx(v[3], v[5]);
+        sel_cx(v[1], v[4]); sel_cx(v[3], v[6]);
+        sel_cx(v[1], v[2]); sel_cx(v[3], v[4]); sel_cx(v[5], v[6]);
+    }
+}
+// a: the eight largest of two descending runs of eight
+__device__ __forceinline__ void sel_merge8(float *a, const float *b)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmaxf(a[i], b[7 - i]);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) sel_cx(a[i], a[i + d]);
+}
 
-    float l[EPT];
+// EPT consecutive logits of a row from e0 (beyond E: -inf)
+template <int EPT, typename LT>
+__device__ __forceinline__ void sel_load_row(const SelectArgs &a, const LT *row, int e0, float (&l)[EPT])
+{
+    constexpr int PV = 16 / (int)sizeof(LT); // values in 16 bytes
     if (EPT % PV == 0 && a.vec && e0 + EPT <= a.E) {
 #pragma unroll
         for (int i = 0; i < EPT / PV; ++i) {
@@ -221,72 +263,108 @@ __global__ void __launch_bounds__(256) route_select_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < EPT; ++i) l[i] = e0 + i < a.E ? sel_load(row + e0 + i) : -INFINITY;
     }
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) l[i] = sel_clean(l[i]);
+}
 
-    const bool biased = a.bias != nullptr;
-    const bool sum2 = a.groups > 1 && a.sum2;
-    // softmax: the row's maximum and sum where anything but the order is needed
-    float m = 0.0f, sum = 1.0f;
-    if (!a.sigmoid && (biased || sum2 || !a.renorm)) {
-        m = l[0];
+// A score in 32 bits: the sigmoid, or exp(l - m) / sum with inv = 1 / sum.
+__device__ __forceinline__ float sel_score(int sigmoid, float l, float m, float inv)
+{
+    return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __expf(l - m) * inv;
+}
+
+// A group's value from its two largest keys (SEL_FAR: none). Without a bias the keys are logits and
+// a sum is formed of their scores (the order is the same).
+__device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biased, float v1, float v2,
+                                                 float m, float inv)
+{
+    if (!a.sum2 || !(v1 > -SEL_EDGE)) return v1;
+    if (biased) return v2 > -SEL_EDGE ? v1 + v2 : v1;
+    return sel_score(a.sigmoid, v1, m, inv) + (v2 > -SEL_EDGE ? sel_score(a.sigmoid, v2, m, inv) : 0.0f);
+}
+
+// Threads per block and blocks per SM (the launch fills the SMs once).
+__host__ __device__ constexpr int sel_threads(int ept) { return ept == 32 ? 128 : 256; }
+__host__ __device__ constexpr int sel_blocks(int ept) { return ept <= 4 ? 4 : ept == 16 ? 2 : 3; }
+
+// Dynamic shared memory, per warp: E 8-byte words (sel_exact's keys; the values of odd-sized
+// groups), then 34 8-byte words (the rounds' winners).
+template <int EPT, typename LT, bool BIASED>
+__global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_select_kernel(const __grid_constant__ SelectArgs a)
+{
+    constexpr bool EXACT = !BIASED && (EPT == 1 || sizeof(LT) == 2); // keys order as 64 bits would
+    constexpr bool IDS = EXACT && EPT > 1;                           // keys carry expert ids
+    constexpr int D = EPT < 8 ? EPT : 8;                             // sorted keys kept per lane
+    constexpr float TOL_KEY = EPT == 1 ? SEL_TOL_KEY : SEL_TOL_KEY + SEL_PLACE(EPT);
+    extern __shared__ unsigned long long sel_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    unsigned long long *scratch = sel_smem + (size_t)warp * (a.E + 34);
+    uint2 *pick = reinterpret_cast<uint2 *>(scratch + a.E);
+    const int T = a.n_rows != nullptr ? min(a.T, *a.n_rows) : a.T;
+    const int e0 = lane * EPT;
+    const uint32_t below = (1u << lane) - 1u;
+    const int step = gridDim.x * warps;
+    int t = blockIdx.x * warps + warp;
+    if (t >= T) return;
+
+    const bool sums = a.groups > 1 && a.sum2;
+    const bool need_sum = !a.sigmoid && (BIASED || sums || !a.renorm);
+    const int lanes = a.groups > 1 ? a.gsz / EPT : 1; // lanes of a group, where it is whole lanes
+    const bool whole = a.groups > 1 && a.gsz % EPT == 0 && (lanes & (lanes - 1)) == 0;
+    const int my_group = whole ? lane / lanes : 0;
+    float bias[BIASED && EPT <= 8 ? EPT : 1];
+    if (BIASED && EPT <= 8) {
 #pragma unroll
-        for (int i = 1; i < EPT; ++i) m = fmaxf(m, l[i]);
-        m = sel_max(m);
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) s += l[i] > -INFINITY ? __expf(l[i] - m) : 0.0f;
-        sum = sel_sum(s);
-        if (sum == 0.0f) sum = 1.0f; // every expert masked
+        for (int i = 0; i < EPT; ++i) bias[i % (int)(sizeof(bias) / 4)] = e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
     }
-    const float inv = 1.0f / sum;
-    float v[EPT]; // key, or s + bias where sums over groups need it
-    if (biased || sum2) {
+    float next[EPT];
+    sel_load_row(a, static_cast<const LT *>(a.logits) + (size_t)t * a.ld, e0, next);
+
+    for (; t < T; t += step) {
+        const LT *row = static_cast<const LT *>(a.logits) + (size_t)t * a.ld;
+        float v[EPT];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            float s = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - m) * inv;
-            if (biased && e0 + i < a.E) s += a.bias[e0 + i];
-            v[i] = s == s ? s : -INFINITY;
-            if (!(l[i] > -INFINITY)) v[i] = -INFINITY;
+        for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(next[i], -SEL_FAR), SEL_FAR); // NaN: masked
+        if (t + step < T) sel_load_row(a, row + (size_t)step * a.ld, e0, next);
+        bool bad = false;
+
+        // softmax: the row's maximum and sum where anything but the order is needed
+        float m = 0.0f, sum = 1.0f;
+        if (need_sum) {
+            m = v[0];
+#pragma unroll
+            for (int i = 1; i < EPT; ++i) m = fmaxf(m, v[i]);
+            m = sel_max(m);
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) s += __expf(v[i] - m);
+            sum = sel_sum(s);
+            bad = !(fabsf(m) < SEL_EDGE);
         }
-    } else {
+        const float inv = __fdividef(1.0f, sum);
+        if (BIASED) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[i] = l[i];
-    }
-    const float tol = a.sigmoid ? SEL_TOL_SIGMOID : SEL_TOL_SOFTMAX * inv;
-    bool clear = true;
+            for (int i = 0; i < EPT; ++i) {
+                const float b = EPT <= 8 ? bias[i % (int)(sizeof(bias) / 4)] : (e0 + i < a.E ? a.bias[e0 + i] : 0.0f);
+                const float key = fminf(fmaxf(sel_score(a.sigmoid, v[i], m, inv) + b, -SEL_FAR), SEL_FAR);
+                v[i] = v[i] > -SEL_EDGE ? key : -SEL_FAR;
+            }
+        }
+        float tol = a.sigmoid ? SEL_TOL_SIGMOID : SEL_TOL_SOFTMAX * inv;
+        if (!BIASED && sums) {
+            // the scores of a group's two largest logits, each off by its place's EPT 2^-23 |l|
+            // through the score's slope: |l| s (1 - s) < 0.23, |l| s < (|m| + 1) / sum
+            tol += (a.sigmoid ? 1.0f : 2.0f * (fabsf(m) + 1.0f) * inv) * SEL_PLACE(EPT);
+        }
 
-    bool stays = true; // this lane's experts (fast form), or bit g of stay_mask
-    uint32_t stay_mask = 0xffffffffu;
-    bool by_mask = false;
-    if (a.groups > 1) {
-        const int lanes = a.gsz / EPT;
-        float gv;
-        if (a.gsz % EPT == 0 && (lanes & (lanes - 1)) == 0) {
-            // a group is `lanes` (a power of two) whole lanes: its two largest by butterflies
-            float v1 = v[0], v2 = -INFINITY;
-#pragma unroll
-            for (int i = 1; i < EPT; ++i) {
-                v2 = fmaxf(v2, fminf(v1, v[i]));
-                v1 = fmaxf(v1, v[i]);
-            }
-            for (int off = 1; off < lanes; off <<= 1) {
-                const float o1 = __shfl_xor_sync(0xffffffffu, v1, off);
-                const float o2 = __shfl_xor_sync(0xffffffffu, v2, off);
-                v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
-                v1 = fmaxf(v1, o1);
-            }
-            gv = (sum2 && v2 > -INFINITY) ? v1 + v2 : v1;
-            gv = __shfl_sync(0xffffffffu, gv, lane < a.groups ? lane * lanes : 0);
-            by_mask = false;
-        } else {
-            // any other size: the values through shared memory, lane g walks group g
+        float gv = 0.0f;
+        uint32_t stay = 0xffffffffu; // odd-sized groups: bit g
+        if (a.groups > 1 && !whole) {
+            // the keys through shared memory, lane g walks group g
             float *sv = reinterpret_cast<float *>(scratch);
 #pragma unroll
             for (int i = 0; i < EPT; ++i)
                 if (e0 + i < a.E) sv[e0 + i] = v[i];
             __syncwarp();
-            float v1 = -INFINITY, v2 = -INFINITY;
+            float v1 = -SEL_FAR, v2 = -SEL_FAR;
             if (lane < a.groups)
                 for (int i = 0; i < a.gsz; ++i) {
                     const float x = sv[lane * a.gsz + i];
@@ -294,86 +372,127 @@ __global__ void __launch_bounds__(256) route_select_kernel(const __grid_constant
                     v1 = fmaxf(v1, x);
                 }
             __syncwarp();
-            gv = (sum2 && v2 > -INFINITY) ? v1 + v2 : v1;
-            by_mask = true;
-        }
-        const bool st = sel_group_stays(gv, a.groups, a.keep, lane);
-        stay_mask = __ballot_sync(0xffffffffu, st);
-        if ((biased || sum2) && a.keep < a.groups) {
-            // the border between the groups that stay and the others
-            const float lo = sel_unord(__reduce_min_sync(0xffffffffu, st ? sel_ord(gv) : 0xffffffffu));
-            const float hi = sel_unord(__reduce_max_sync(
-                0xffffffffu, (!st && lane < a.groups) ? sel_ord(gv) : SEL_NEG_INF));
-            const float bound = 2.0f * tol + SEL_TOL_KEY * (fabsf(lo) + fabsf(hi));
-            if (hi > -INFINITY && !(lo - hi > bound)) clear = false;
-        }
-        if (!by_mask) stays = (stay_mask >> min(e0 / a.gsz, 31)) & 1u;
-    }
-
-    uint32_t o[EPT];
-    uint32_t best = 0;
+            gv = sel_group_value(a, BIASED, v1, v2, m, inv);
+            const bool st = sel_group_stays(gv, a.groups, a.keep, lane);
+            stay = __ballot_sync(0xffffffffu, st);
+            const float lo = sel_min(st ? gv : SEL_FAR), hi = sel_max(!st && lane < a.groups ? gv : -SEL_FAR);
+            if ((BIASED || sums) && hi > -SEL_FAR && !(lo - hi > 2.0f * tol + SEL_TOL_KEY * (fabsf(lo) + fabsf(hi))))
+                bad = true;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-        const bool live = l[i] > -INFINITY;
-        o[i] = live ? sel_ord(biased ? v[i] : l[i]) : SEL_MASKED;
-        bool cand = stays && e0 + i < a.E;
-        if (by_mask && cand) cand = (stay_mask >> ((e0 + i) / a.gsz)) & 1u;
-        if (!cand) o[i] = 0;
-        best = max(best, o[i]);
-    }
-
-    int mine = 0;
-    float prev = 0.0f;
-    const int rounds = biased ? a.k + 1 : a.k;
-    for (int j = 0; j < rounds && clear; ++j) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const int src = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-        if (biased) {
-            const float cur = sel_unord(top);
-            if (j > 0 && top > SEL_NEG_INF && !(prev - cur > tol + SEL_TOL_KEY * (fabsf(prev) + fabsf(cur))))
-                clear = false;
-            prev = cur;
+            for (int i = 0; i < EPT; ++i)
+                if (!((stay >> min((e0 + i) / a.gsz, 31)) & 1u)) v[i] = -SEL_FAR;
         }
-        int e = 0;
-        if (lane == src) {
-            uint32_t nb = 0;
-            bool found = false;
+
+        // the place (or id) into the lowest bits, then each lane's keys in descending order
+        if (IDS) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                if (!found && o[i] == top) {
-                    found = true;
-                    e = e0 + i;
-                    o[i] = 0;
-                }
-                nb = max(nb, o[i]);
+            for (int i = 0; i < EPT; ++i) { // larger bits are larger for a positive key only
+                const uint32_t u = __float_as_uint(v[i] + 0.0f) & 0xffff0000u;
+                v[i] = __uint_as_float(u | (uint32_t)((u >> 31) ? e0 + i : 1023 - e0 - i));
             }
-            best = nb;
+        } else if (EPT > 1) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+                v[i] = __uint_as_float((__float_as_uint(v[i]) & ~(uint32_t)(EPT - 1)) | (uint32_t)i);
         }
-        e = __shfl_sync(0xffffffffu, e, src);
-        if (lane == j) mine = e;
-    }
-    if (!clear) mine = sel_exact(a, row, scratch, lane);
+        if constexpr (EPT <= 8) {
+            sel_sort<EPT>(v);
+        } else {
+#pragma unroll
+            for (int c = 0; c < EPT / 8; ++c) sel_sort<8>(v + 8 * c);
+#pragma unroll
+            for (int c = 1; c < EPT / 8; ++c) sel_merge8(v, v + 8 * c);
+        }
 
-    // weights, once for the k selected on lanes 0 .. k - 1
-    const bool on = lane < a.k;
-    const float lj = on ? sel_clean(sel_load(row + mine)) : -INFINITY;
-    const bool live = lj > -INFINITY;
-    float u = 0.0f;
-    if (a.sigmoid) {
-        const float mn = fminf(lj, 0.0f);
-        const float M = a.renorm ? sel_max(live ? mn : -INFINITY) : 0.0f; // keeps tiny scores' ratios
-        if (live) u = expf(mn - M) / (1.0f + expf(-fabsf(lj)));
-    } else {
-        const float M = a.renorm ? sel_max(lj) : m;
-        if (live) u = a.renorm ? expf(lj - M) : expf(lj - M) / sum;
-    }
-    if (a.renorm) {
-        const float total = sel_sum(u);
-        u = total > 0.0f ? u / total : 0.0f;
-    }
-    if (on) {
-        a.idx[(size_t)t * a.k + lane] = mine;
-        a.w[(size_t)t * a.k + lane] = a.scale * u;
+        if (whole) {
+            float v1 = v[0], v2 = EPT > 1 ? v[EPT > 1 ? 1 : 0] : -SEL_FAR;
+            if (IDS) {
+                v1 = __uint_as_float(__float_as_uint(v1) & 0xffff0000u);
+                v2 = __uint_as_float(__float_as_uint(v2) & 0xffff0000u);
+            }
+            for (int off = 1; off < lanes; off <<= 1) {
+                const float o1 = __shfl_xor_sync(0xffffffffu, v1, off);
+                const float o2 = __shfl_xor_sync(0xffffffffu, v2, off);
+                v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
+                v1 = fmaxf(v1, o1);
+            }
+            gv = sel_group_value(a, BIASED, v1, v2, m, inv);
+            // the group's rank: its lanes compare with the groups c, c + lanes, ... and add up
+            int rank = 0;
+            for (int g0 = 0; g0 < a.groups; g0 += lanes) { // every lane takes every turn
+                const int g = g0 + (lane & (lanes - 1));
+                const float o = __shfl_sync(0xffffffffu, gv, min(g, a.groups - 1) * lanes);
+                if (g < a.groups) rank += (o > gv || (o == gv && g < my_group)) ? 1 : 0;
+            }
+            for (int off = 1; off < lanes; off <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, off);
+            const bool in = my_group < a.groups, st = in && rank < a.keep;
+            if (!EXACT || sums) {
+                const float lo = sel_min(st ? gv : SEL_FAR), hi = sel_max(in && !st ? gv : -SEL_FAR);
+                if (hi > -SEL_EDGE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) + TOL_KEY * (fabsf(lo) + fabsf(hi)) + SEL_TOL_ZERO))
+                    bad = true;
+            }
+            if (!st) v[0] = -SEL_FAR;
+        }
+
+        const int rounds = EXACT ? a.k : a.k + 1; // one more: the best that is left out
+#pragma unroll 1
+        for (int j = 0; j < rounds; ++j) {
+            const float top = sel_max(v[0]);
+            const bool head = v[0] == top;
+            const uint32_t all = __ballot_sync(0xffffffffu, head);
+            if (head && !(all & below)) {
+                pick[j] = make_uint2(__float_as_uint(top), (uint32_t)lane);
+#pragma unroll
+                for (int i = 0; i + 1 < D; ++i) v[i] = v[i + 1];
+                // a lane that gave all its experts has no more; one that kept eight of more might
+                v[D - 1] = EPT > D ? SEL_FAR : -SEL_FAR;
+            }
+        }
+        __syncwarp();
+        int mine = 0;
+        const bool on = lane < a.k;
+        if (on) {
+            const uint2 p = pick[lane];
+            const float key = __uint_as_float(p.x);
+            if (!(fabsf(key) < SEL_EDGE)) bad = true;
+            if (!EXACT) {
+                const float after = __uint_as_float(pick[lane + 1].x);
+                if (!(key - after > (BIASED ? tol : 0.0f) + TOL_KEY * (fabsf(key) + fabsf(after)) + SEL_TOL_ZERO)) bad = true;
+            }
+            if (IDS)
+                mine = (p.x >> 31) ? (int)(p.x & 0xffffu) : 1023 - (int)(p.x & 0xffffu);
+            else
+                mine = (int)p.y * EPT + (EPT > 1 ? (int)(p.x & (uint32_t)(EPT - 1)) : 0);
+        }
+        __syncwarp(); // pick and scratch are free for the next token
+        if (__any_sync(0xffffffffu, bad)) {
+            const SelExact x = sel_exact(a, row, scratch, lane);
+            mine = x.mine;
+            m = x.m;
+            sum = x.sum;
+            __syncwarp();
+        }
+
+        // weights, once for the k selected on lanes 0 .. k - 1
+        const float lj = on ? sel_clean(sel_load(row + mine)) : -INFINITY;
+        const bool live = lj > -INFINITY;
+        float u = 0.0f;
+        if (a.sigmoid) {
+            const float mn = fminf(lj, 0.0f);
+            const float M = a.renorm ? sel_max(live ? mn : -INFINITY) : 0.0f; // keeps tiny scores' ratios
+            if (live) u = __fdividef(expf(mn - M), 1.0f + expf(-fabsf(lj)));
+        } else {
+            const float M = a.renorm ? sel_max(lj) : m;
+            if (live) u = a.renorm ? expf(lj - M) : __fdividef(expf(lj - M), sum);
+        }
+        if (a.renorm) {
+            const float total = sel_sum(u);
+            u = total > 0.0f ? __fdividef(u, total) : 0.0f;
+        }
+        if (on) {
+            a.idx[(size_t)t * a.k + lane] = mine;
+            a.w[(size_t)t * a.k + lane] = a.scale * u;
+        }
     }
 }
 
