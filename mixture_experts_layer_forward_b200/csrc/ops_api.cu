@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 
 #include "dropout.cuh"
 #include "host.cuh"
@@ -42,25 +43,46 @@ moe_status check_select(const moe_select *s)
 int dtype_bytes(int32_t d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 bool aligned_to(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % (unsigned)bytes) == 0; }
 
-template <int EPT, typename LT, bool BIASED>
+std::atomic<int> g_select_wide{getenv("SELW") ? atoi(getenv("SELW")) : 2048};
+
+template <int LPT, int EPT, typename LT, bool BIASED>
 cudaError_t launch_select(const SelectArgs &a, cudaStream_t st)
 {
-    constexpr int warps = sel_threads(EPT) / 32; // the scratch stays within 48 KB
-    const size_t smem = (size_t)warps * (a.E + 34) * sizeof(unsigned long long);
+    constexpr int warps = sel_threads(LPT, EPT) / 32, per_block = warps * (32 / LPT);
+    const int smem = sel_smem(LPT, EPT, warps, a.E, BIASED);
+    static_assert(sel_smem(LPT, EPT, warps, LPT * EPT, BIASED) <= 48 * 1024, "no opt-in needed");
     const int sms = sm_count() > 0 ? sm_count() : 148;
-    const unsigned grid = (unsigned)std::min((a.T + warps - 1) / warps, sms * sel_blocks(EPT));
-    route_select_kernel<EPT, LT, BIASED><<<grid, warps * 32, smem, st>>>(a);
+    const int64_t blocks = ((int64_t)a.T + per_block - 1) / per_block;
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * sel_blocks(LPT, EPT));
+    route_select_kernel<LPT, EPT, LT, BIASED><<<grid, warps * 32, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename LT, bool BIASED> cudaError_t launch_select_wide(const SelectArgs &a, cudaStream_t st)
 {
-    if (a.E <= 32) return launch_select<1, LT, BIASED>(a, st);
-    if (a.E <= 64) return launch_select<2, LT, BIASED>(a, st);
-    if (a.E <= 128) return launch_select<4, LT, BIASED>(a, st);
-    if (a.E <= 256) return launch_select<8, LT, BIASED>(a, st);
-    if (a.E <= 512) return launch_select<16, LT, BIASED>(a, st);
-    return launch_select<32, LT, BIASED>(a, st);
+    // Four tokens per warp where they fit (k <= 8, E <= 256, groups of whole lanes) and there are
+    // enough of them
+    int ept = 1;
+    while (ept * 8 < a.E) ept *= 2;
+    const int lanes = a.gsz / ept;
+    const bool fits = a.k <= 8 && a.E <= 256 &&
+                      (a.groups == 1 || (a.gsz % ept == 0 && (lanes & (lanes - 1)) == 0));
+    if (fits && a.T >= g_select_wide.load()) {
+        switch (ept) {
+        case 1: return launch_select<8, 1, LT, BIASED>(a, st);
+        case 2: return launch_select<8, 2, LT, BIASED>(a, st);
+        case 4: return launch_select<8, 4, LT, BIASED>(a, st);
+        case 8: return launch_select<8, 8, LT, BIASED>(a, st);
+        case 16: return launch_select<8, 16, LT, BIASED>(a, st);
+        default: return launch_select<8, 32, LT, BIASED>(a, st);
+        }
+    }
+    if (a.E <= 32) return launch_select<32, 1, LT, BIASED>(a, st);
+    if (a.E <= 64) return launch_select<32, 2, LT, BIASED>(a, st);
+    if (a.E <= 128) return launch_select<32, 4, LT, BIASED>(a, st);
+    if (a.E <= 256) return launch_select<32, 8, LT, BIASED>(a, st);
+    if (a.E <= 512) return launch_select<32, 16, LT, BIASED>(a, st);
+    return launch_select<32, 32, LT, BIASED>(a, st);
 }
 
 template <typename LT> cudaError_t launch_select_any(const SelectArgs &a, cudaStream_t st)

@@ -41,8 +41,8 @@ constexpr int SEL_MAX_K = 32;      // one selected expert per lane
 constexpr int SEL_MAX_GROUPS = 32; // one group per lane
 
 // Bounds on the gap of two 32-bit keys whose 64-bit order could differ (both keys' errors):
-// sigmoid: the exponential's (2 + 1.17 |l|) ulp through s (1 - s) is at most 7.5e-8, the sum
-//   1 + e adds 2^-24 s, the quotient 2 ulp: 3.8e-7 a key, 7.6e-7 for two;
+// sigmoid: e = 2^(-l log2 e) is off by 2^-22.5 + 1.5 |l| 2^-24 of itself, which s (1 - s) takes to
+//   at most 6.3e-8; the sum 1 + e adds 2^-24 s, the reciprocal 2^-23 s: 2.5e-7 a key, 5e-7 for two;
 // softmax: 3.2e-7 s_max a key from the exponential, and one factor common to all keys (the sum:
 //   36 rounded additions and the terms' own errors, the reciprocal) of at most 4.1e-6: 4.8e-6;
 // the sum with the bias rounds by 2^-24 of the key, the place by at most EPT 2^-23 of it.
@@ -93,15 +93,25 @@ constexpr unsigned long long SEL_MASKED = 1ull;
 __device__ __forceinline__ float sel_max(float v)
 {
     float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ float sel_min(float v)
+// 2^x and 1 / x as the special function unit gives them (2^-22.5 and 2^-23 relative, denormal
+// results 0)
+__device__ __forceinline__ float sel_ex2(float x)
 {
     float r;
-    asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float sel_rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float SEL_LOG2E = 1.4426950408889634f;
+
 __device__ __forceinline__ float sel_sum(float v)
 {
 #pragma unroll
@@ -122,10 +132,39 @@ __device__ __forceinline__ bool sel_group_stays(V gv, int groups, int keep, int 
     return lane < groups && rank < keep;
 }
 
+// s + bias of a sigmoid score in 64 bits (a NaN bias: -inf)
+__device__ __noinline__ double sel_value64(float l, float b)
+{
+    const double v = 1.0 / (1.0 + exp(-(double)l)) + (double)b;
+    return v == v ? v : -INFINITY;
+}
+
 struct SelExact {
     int mine;     // the expert selected in round `lane` (lane < k)
     float m, sum; // softmax: the row's maximum and sum
 };
+
+// Over the LPT lanes of a token.
+template <int LPT> __device__ __forceinline__ float sel_max_of(float v)
+{
+    if constexpr (LPT == 32) {
+        return sel_max(v);
+    } else {
+#pragma unroll
+        for (int off = LPT / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+        return v;
+    }
+}
+template <int LPT> __device__ __forceinline__ float sel_min_of(float v)
+{
+    return -sel_max_of<LPT>(-v);
+}
+template <int LPT> __device__ __forceinline__ float sel_sum_of(float v)
+{
+#pragma unroll
+    for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
 
 // The selection with keys in 64 bits. key: E order words of this warp in shared memory.
 template <typename LT>
@@ -145,62 +184,80 @@ __device__ __noinline__ SelExact sel_exact(const SelectArgs &a, const LT *row, u
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
     auto value = [&](float l, int e) -> double { // s + bias of a live expert
-        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - m) / sum;
-        const double v = a.bias != nullptr ? s + (double)a.bias[e] : s;
+        const float b = a.bias != nullptr ? a.bias[e] : 0.0f;
+        if (a.sigmoid) return sel_value64(l, b);
+        const double v = exp((double)l - m) / sum + (double)b;
         return v == v ? v : -INFINITY;
     };
+    // first the values (s + bias; without a bias and sums, the logits), for the groups
+    const bool plain = a.bias == nullptr && !a.sum2;
     uint32_t stay = 0xffffffffu;
     if (a.groups > 1) {
-        double gv = -INFINITY;
-        if (lane < a.groups) {
-            double v1 = -INFINITY, v2 = -INFINITY;
-            for (int i = 0; i < a.gsz; ++i) {
-                const int e = lane * a.gsz + i;
-                const float l = sel_clean(sel_load(row + e));
-                if (!(l > -INFINITY)) continue;
-                const double v = (a.bias != nullptr || a.sum2) ? value(l, e) : (double)l;
-                if (v > v1) {
-                    v2 = v1;
-                    v1 = v;
-                } else if (v > v2) {
-                    v2 = v;
-                }
-            }
-            gv = (a.sum2 && v2 > -INFINITY) ? v1 + v2 : v1;
+        double *val = reinterpret_cast<double *>(key);
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) {
+            const float l = sel_clean(sel_load(row + e));
+            val[e] = !(l > -INFINITY) ? -INFINITY : plain ? (double)l : value(l, e);
         }
+        __syncwarp();
+        // `per` lanes (a power of two) walk a group's values, then add their findings
+        int per = 1;
+        while (per * 2 * a.groups <= 32) per *= 2;
+        const int g = lane / per;
+        double v1 = -INFINITY, v2 = -INFINITY;
+        if (g < a.groups)
+            for (int i = lane & (per - 1); i < a.gsz; i += per) {
+                const double v = val[g * a.gsz + i];
+                v2 = fmax(v2, fmin(v1, v));
+                v1 = fmax(v1, v);
+            }
+        for (int off = 1; off < per; off <<= 1) {
+            const double o1 = __shfl_xor_sync(0xffffffffu, v1, off);
+            const double o2 = __shfl_xor_sync(0xffffffffu, v2, off);
+            v2 = fmax(fmin(v1, o1), fmax(v2, o2));
+            v1 = fmax(v1, o1);
+        }
+        double gv = (a.sum2 && v2 > -INFINITY) ? v1 + v2 : v1;
+        gv = __shfl_sync(0xffffffffu, gv, min(lane * per, 31)); // lane g: group g's
         stay = __ballot_sync(0xffffffffu, sel_group_stays(gv, a.groups, a.keep, lane));
+        __syncwarp();
     }
+    // then the order words; a lane's experts are lane, lane + 32, ...
+    unsigned long long bo = 0;
+    int be = lane;
+#pragma unroll 1
     for (int e = lane; e < a.E; e += 32) {
         const float l = sel_clean(sel_load(row + e));
         unsigned long long o = SEL_MASKED;
-        if (l > -INFINITY) o = sel_ord64(a.bias != nullptr ? value(l, e) : (double)l);
+        if (l > -INFINITY)
+            o = sel_ord64(a.bias == nullptr ? (double)l
+                          : a.groups > 1    ? reinterpret_cast<double *>(key)[e]
+                                            : value(l, e));
         if (a.groups > 1 && !((stay >> (e / a.gsz)) & 1u)) o = 0;
         key[e] = o;
+        if (o > bo) {
+            bo = o;
+            be = e;
+        }
     }
-    __syncwarp();
     int mine = 0;
     for (int j = 0; j < a.k; ++j) {
-        unsigned long long bo = 0;
-        int be = 0x7fffffff;
-        for (int e = lane; e < a.E; e += 32)
-            if (key[e] > bo) {
-                bo = key[e];
-                be = e;
-            }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const unsigned long long oo = __shfl_xor_sync(0xffffffffu, bo, off);
-            const int oe = __shfl_xor_sync(0xffffffffu, be, off);
-            if (oo > bo || (oo == bo && oe < be)) {
-                bo = oo;
-                be = oe;
-            }
+        // the largest word, its two halves in turn, then the lowest id that has it
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(bo >> 32));
+        const bool h = (uint32_t)(bo >> 32) == hi;
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, h ? (uint32_t)bo : 0u);
+        const int win = (int)__reduce_min_sync(0xffffffffu, h && (uint32_t)bo == lo ? (uint32_t)be : 0x7fffffffu);
+        if (lane == j) mine = win;
+        if (be == win) { // its lane looks for its next
+            key[win] = 0;
+            bo = 0;
+            for (int e = lane; e < a.E; e += 32)
+                if (key[e] > bo) {
+                    bo = key[e];
+                    be = e;
+                }
+            if (bo == 0) be = lane;
         }
-        if (be >= a.E) be = 0; // not reached: at least k experts are candidates
-        if (lane == j) mine = be;
-        __syncwarp();
-        if (lane == 0) key[be] = 0;
-        __syncwarp();
     }
     return SelExact{mine, (float)m, sum > 0.0 ? (float)sum : 1.0f};
 }
@@ -265,10 +322,20 @@ __device__ __forceinline__ void sel_load_row(const SelectArgs &a, const LT *row,
     }
 }
 
+// a finite bias: beyond SEL_EDGE sel_exact decides (a NaN bias counts as -inf)
+__device__ __forceinline__ float sel_bias(float b) { return fminf(fmaxf(b, -SEL_FAR), SEL_FAR); }
+
+// the expert id that an IDS key carries
+__device__ __forceinline__ int sel_id(float key)
+{
+    const uint32_t u = __float_as_uint(key);
+    return (u >> 31) ? (int)(u & 0xffffu) : 1023 - (int)(u & 0xffffu);
+}
+
 // A score in 32 bits: the sigmoid, or exp(l - m) / sum with inv = 1 / sum.
 __device__ __forceinline__ float sel_score(int sigmoid, float l, float m, float inv)
 {
-    return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __expf(l - m) * inv;
+    return sigmoid ? sel_rcp(1.0f + sel_ex2(l * -SEL_LOG2E)) : sel_ex2((l - m) * SEL_LOG2E) * inv;
 }
 
 // A group's value from its two largest keys (SEL_FAR: none). Without a bias the keys are logits and
@@ -282,48 +349,98 @@ __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biase
 }
 
 // Threads per block and blocks per SM (the launch fills the SMs once).
-__host__ __device__ constexpr int sel_threads(int ept) { return ept == 32 ? 128 : 256; }
-__host__ __device__ constexpr int sel_blocks(int ept) { return ept <= 4 ? 4 : ept == 16 ? 2 : 3; }
+__host__ __device__ constexpr int sel_threads(int lpt, int ept) { return lpt == 32 && ept == 32 ? 128 : 256; }
+__host__ __device__ constexpr int sel_blocks(int lpt, int ept)
+{
+    return lpt == 8 ? 4 : ept <= 4 ? 4 : ept == 16 ? 2 : 3;
+}
+// The bias in shared memory: lane i's EPT values, then (from 4) 4 more, so that 16-byte reads of
+// eight lanes meet no bank twice.
+__host__ __device__ constexpr int sel_bias_ld(int ept) { return ept >= 4 ? ept + 4 : ept; }
+// Per warp: 8-byte words of scratch (64-bit keys; the values of odd-sized groups; with LPT = 8 and
+// EPT >= 4 the rows of its four tokens, laid out as the bias), then 40 of the rounds' winners (up to
+// LPT + 2 per token).
+__host__ __device__ constexpr int sel_scratch(int lpt, int ept, int E)
+{
+    const int rows = lpt == 8 && ept >= 4 ? 16 * sel_bias_ld(ept) : 40; // 4 tokens x 8 lanes x ld floats
+    return rows > E ? rows : E; // at least 40: the winners' 64-bit keys
+}
+__host__ __device__ constexpr int sel_smem(int lpt, int ept, int warps, int E, bool biased)
+{
+    return (biased ? lpt * sel_bias_ld(ept) * 4 : 0) + warps * (sel_scratch(lpt, ept, E + (E & 1)) + 40) * 8;
+}
 
-// Dynamic shared memory, per warp: E 8-byte words (sel_exact's keys; the values of odd-sized
-// groups), then 34 8-byte words (the rounds' winners).
-template <int EPT, typename LT, bool BIASED>
-__global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_select_kernel(const __grid_constant__ SelectArgs a)
+// LPT lanes per token (32, or 8: four tokens per warp), E <= LPT * EPT, k <= LPT. With LPT = 8 groups are
+// whole lanes, a power of two of them, or there are none.
+template <int LPT, int EPT, typename LT, bool BIASED>
+__global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
+    route_select_kernel(const __grid_constant__ SelectArgs a)
 {
     constexpr bool EXACT = !BIASED && (EPT == 1 || sizeof(LT) == 2); // keys order as 64 bits would
     constexpr bool IDS = EXACT && EPT > 1;                           // keys carry expert ids
     constexpr int D = EPT < 8 ? EPT : 8;                             // sorted keys kept per lane
     constexpr float TOL_KEY = EPT == 1 ? SEL_TOL_KEY : SEL_TOL_KEY + SEL_PLACE(EPT);
-    extern __shared__ unsigned long long sel_smem[];
+    constexpr int BLD = sel_bias_ld(EPT);
+    extern __shared__ uint4 sel_smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    unsigned long long *scratch = sel_smem + (size_t)warp * (a.E + 34);
-    uint2 *pick = reinterpret_cast<uint2 *>(scratch + a.E);
+    float *sbias = reinterpret_cast<float *>(sel_smem_raw);
+    const int nscratch = sel_scratch(LPT, EPT, a.E + (a.E & 1)); // even: 16-byte rows
+    unsigned long long *scratch =
+        reinterpret_cast<unsigned long long *>(sbias + (BIASED ? LPT * BLD : 0)) + (size_t)warp * (nscratch + 40);
+    const int sl = lane & (LPT - 1), seg = lane / LPT;
+    uint2 *pick = reinterpret_cast<uint2 *>(scratch + nscratch) + seg * (LPT + 2);
     const int T = a.n_rows != nullptr ? min(a.T, *a.n_rows) : a.T;
-    const int e0 = lane * EPT;
-    const uint32_t below = (1u << lane) - 1u;
-    const int step = gridDim.x * warps;
-    int t = blockIdx.x * warps + warp;
-    if (t >= T) return;
-
+    const int e0 = sl * EPT;
+    const uint32_t rivals = ((1u << lane) - 1u) & (LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1u) << (seg * LPT));
+    if (BIASED) {
+        for (int e = threadIdx.x; e < LPT * EPT; e += blockDim.x)
+            sbias[e / EPT * BLD + e % EPT] = e < a.E ? sel_bias(a.bias[e]) : 0.0f;
+        __syncthreads();
+    }
     const bool sums = a.groups > 1 && a.sum2;
     const bool need_sum = !a.sigmoid && (BIASED || sums || !a.renorm);
     const int lanes = a.groups > 1 ? a.gsz / EPT : 1; // lanes of a group, where it is whole lanes
-    const bool whole = a.groups > 1 && a.gsz % EPT == 0 && (lanes & (lanes - 1)) == 0;
-    const int my_group = whole ? lane / lanes : 0;
-    float bias[BIASED && EPT <= 8 ? EPT : 1];
-    if (BIASED && EPT <= 8) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) bias[i % (int)(sizeof(bias) / 4)] = e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
-    }
-    float next[EPT];
-    sel_load_row(a, static_cast<const LT *>(a.logits) + (size_t)t * a.ld, e0, next);
+    const bool whole = a.groups > 1 && (LPT == 8 || (a.gsz % EPT == 0 && (lanes & (lanes - 1)) == 0));
+    const int my_group = whole ? sl / lanes : 0;
+    constexpr int TPW = 32 / LPT; // tokens per warp
 
-    for (; t < T; t += step) {
+    for (int64_t tw = (int64_t)(blockIdx.x * warps + warp) * TPW; tw < T; tw += (int64_t)gridDim.x * warps * TPW) {
+        const int t = (int)min(tw + seg, (int64_t)T - 1); // the last warp's spare lanes repeat a token
+        const bool mine_too = tw + seg < T;
         const LT *row = static_cast<const LT *>(a.logits) + (size_t)t * a.ld;
         float v[EPT];
+        if (LPT == 8 && EPT >= 4 && sizeof(LT) == 4 && a.vec && a.E == LPT * EPT) {
+            // four whole fp32 rows, 512 consecutive bytes a time, through shared memory (a lane's own
+            // values are EPT * 4 bytes apart from its neighbour's: 32 lines per load instead of 4)
+            constexpr int Q = EPT >= 4 ? EPT / 4 : 1; // 16-byte pieces of a lane's values
+            float *st = reinterpret_cast<float *>(scratch);
+            float4 x[EPT >= 4 ? EPT / 4 : 1];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(next[i], -SEL_FAR), SEL_FAR); // NaN: masked
-        if (t + step < T) sel_load_row(a, row + (size_t)step * a.ld, e0, next);
+            for (int i = 0; i < Q; ++i) {
+                const int piece = i * 32 + lane, tok = piece / (8 * Q), at = piece % (8 * Q);
+                const int tr = (int)min(tw + tok, (int64_t)T - 1);
+                x[i] = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + (size_t)tr * a.ld)[at];
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int piece = i * 32 + lane, tok = piece / (8 * Q), at = piece % (8 * Q);
+                *reinterpret_cast<float4 *>(st + (tok * 8 + at / Q) * BLD + at % Q * 4) = x[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float4 y = *reinterpret_cast<const float4 *>(st + lane * BLD + i * 4);
+                v[(i * 4) % EPT] = y.x; v[(i * 4 + 1) % EPT] = y.y;
+                v[(i * 4 + 2) % EPT] = y.z; v[(i * 4 + 3) % EPT] = y.w;
+            }
+            __syncwarp();
+        } else {
+            sel_load_row(a, row, e0, v);
+        }
+        if (!(BIASED && a.sigmoid)) { // NaN: masked (a sigmoid and the test of its key need no clamp)
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(v[i], -SEL_FAR), SEL_FAR);
+        }
         bool bad = false;
 
         // softmax: the row's maximum and sum where anything but the order is needed
@@ -332,20 +449,34 @@ __global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_selec
             m = v[0];
 #pragma unroll
             for (int i = 1; i < EPT; ++i) m = fmaxf(m, v[i]);
-            m = sel_max(m);
+            m = sel_max_of<LPT>(m);
             float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) s += __expf(v[i] - m);
-            sum = sel_sum(s);
+            for (int i = 0; i < EPT; ++i) s += sel_ex2((v[i] - m) * SEL_LOG2E);
+            sum = sel_sum_of<LPT>(s);
             bad = !(fabsf(m) < SEL_EDGE);
         }
-        const float inv = __fdividef(1.0f, sum);
+        const float inv = sel_rcp(sum);
         if (BIASED) {
+            float b[EPT];
+            if constexpr (EPT >= 4) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const float b = EPT <= 8 ? bias[i % (int)(sizeof(bias) / 4)] : (e0 + i < a.E ? a.bias[e0 + i] : 0.0f);
-                const float key = fminf(fmaxf(sel_score(a.sigmoid, v[i], m, inv) + b, -SEL_FAR), SEL_FAR);
-                v[i] = v[i] > -SEL_EDGE ? key : -SEL_FAR;
+                for (int i = 0; i < EPT; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(sbias + sl * BLD + i);
+                    b[i] = x.x; b[i + 1] = x.y; b[i + 2] = x.z; b[i + 3] = x.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) b[i] = sbias[sl * BLD + i];
+            }
+            if (a.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    v[i] = v[i] > -SEL_EDGE ? sel_rcp(1.0f + sel_ex2(v[i] * -SEL_LOG2E)) + b[i] : -SEL_FAR;
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    v[i] = v[i] > -SEL_EDGE ? sel_ex2((v[i] - m) * SEL_LOG2E) * inv + b[i] : -SEL_FAR;
             }
         }
         float tol = a.sigmoid ? SEL_TOL_SIGMOID : SEL_TOL_SOFTMAX * inv;
@@ -355,10 +486,8 @@ __global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_selec
             tol += (a.sigmoid ? 1.0f : 2.0f * (fabsf(m) + 1.0f) * inv) * SEL_PLACE(EPT);
         }
 
-        float gv = 0.0f;
-        uint32_t stay = 0xffffffffu; // odd-sized groups: bit g
-        if (a.groups > 1 && !whole) {
-            // the keys through shared memory, lane g walks group g
+        if (LPT == 32 && a.groups > 1 && !whole) {
+            // groups of any other size: the keys through shared memory, lane g walks group g
             float *sv = reinterpret_cast<float *>(scratch);
 #pragma unroll
             for (int i = 0; i < EPT; ++i)
@@ -372,10 +501,11 @@ __global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_selec
                     v1 = fmaxf(v1, x);
                 }
             __syncwarp();
-            gv = sel_group_value(a, BIASED, v1, v2, m, inv);
+            const float gv = sel_group_value(a, BIASED, v1, v2, m, inv);
             const bool st = sel_group_stays(gv, a.groups, a.keep, lane);
-            stay = __ballot_sync(0xffffffffu, st);
-            const float lo = sel_min(st ? gv : SEL_FAR), hi = sel_max(!st && lane < a.groups ? gv : -SEL_FAR);
+            const uint32_t stay = __ballot_sync(0xffffffffu, st);
+            const float lo = sel_min_of<LPT>(st ? gv : SEL_FAR);
+            const float hi = sel_max_of<LPT>(!st && lane < a.groups ? gv : -SEL_FAR);
             if ((BIASED || sums) && hi > -SEL_FAR && !(lo - hi > 2.0f * tol + SEL_TOL_KEY * (fabsf(lo) + fabsf(hi))))
                 bad = true;
 #pragma unroll
@@ -399,9 +529,10 @@ __global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_selec
             sel_sort<EPT>(v);
         } else {
 #pragma unroll
-            for (int c = 0; c < EPT / 8; ++c) sel_sort<8>(v + 8 * c);
-#pragma unroll
-            for (int c = 1; c < EPT / 8; ++c) sel_merge8(v, v + 8 * c);
+            for (int c = 0; c < EPT / 8; ++c) {
+                sel_sort<8>(v + 8 * c);
+                if (c > 0) sel_merge8(v, v + 8 * c);
+            }
         }
 
         if (whole) {
@@ -416,82 +547,174 @@ __global__ void __launch_bounds__(sel_threads(EPT), sel_blocks(EPT)) route_selec
                 v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
                 v1 = fmaxf(v1, o1);
             }
-            gv = sel_group_value(a, BIASED, v1, v2, m, inv);
+            const float gv = sel_group_value(a, BIASED, v1, v2, m, inv);
             // the group's rank: its lanes compare with the groups c, c + lanes, ... and add up
-            int rank = 0;
-            for (int g0 = 0; g0 < a.groups; g0 += lanes) { // every lane takes every turn
-                const int g = g0 + (lane & (lanes - 1));
-                const float o = __shfl_sync(0xffffffffu, gv, min(g, a.groups - 1) * lanes);
-                if (g < a.groups) rank += (o > gv || (o == gv && g < my_group)) ? 1 : 0;
-            }
-            for (int off = 1; off < lanes; off <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, off);
-            const bool in = my_group < a.groups, st = in && rank < a.keep;
+            auto rank_of = [&](auto x) {
+                int rank = 0;
+                for (int g0 = 0; g0 < a.groups; g0 += lanes) { // every lane takes every turn
+                    const int g = g0 + (sl & (lanes - 1));
+                    const auto o = __shfl_sync(0xffffffffu, x, min(g, a.groups - 1) * lanes, LPT);
+                    if (g < a.groups) rank += (o > x || (o == x && g < my_group)) ? 1 : 0;
+                }
+                for (int off = 1; off < lanes; off <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, off);
+                return rank;
+            };
+            const bool in = my_group < a.groups;
+            const int rank = rank_of(gv); // every lane takes part, its group real or not
+            bool st = in && rank < a.keep;
             if (!EXACT || sums) {
-                const float lo = sel_min(st ? gv : SEL_FAR), hi = sel_max(in && !st ? gv : -SEL_FAR);
-                if (hi > -SEL_EDGE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) + TOL_KEY * (fabsf(lo) + fabsf(hi)) + SEL_TOL_ZERO))
-                    bad = true;
+                const float lo = sel_min_of<LPT>(st ? gv : SEL_FAR), hi = sel_max_of<LPT>(in && !st ? gv : -SEL_FAR);
+                const bool close = hi > -SEL_EDGE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) +
+                                                                     TOL_KEY * (fabsf(lo) + fabsf(hi)) + SEL_TOL_ZERO);
+                if (__any_sync(0xffffffffu, close)) {
+                    // the groups' values again in 64 bits, from each lane's two largest (which are its two
+                    // largest in 64 bits too, or the token goes to sel_exact)
+                    const float third = EPT > 2 ? v[EPT > 2 ? 2 : 0] : -SEL_FAR;
+                    const float second = EPT > 1 ? v[EPT > 1 ? 1 : 0] : -SEL_FAR;
+                    const bool sure = !(third > -SEL_EDGE) ||
+                                      second - third > tol + TOL_KEY * (fabsf(second) + fabsf(third)) + SEL_TOL_ZERO;
+                    auto value = [&](float key) -> double {
+                        if (!(key > -SEL_EDGE)) return -INFINITY;
+                        const int e = IDS ? sel_id(key) : e0 + (EPT > 1 ? (int)(__float_as_uint(key) & (uint32_t)(EPT - 1)) : 0);
+                        const float l = sel_load(row + e);
+                        return BIASED || sums ? sel_value64(l, BIASED ? a.bias[e] : 0.0f) : (double)l;
+                    };
+                    double d1 = value(v[0]), d2 = value(second);
+                    if (d2 > d1) {
+                        const double x = d1;
+                        d1 = d2;
+                        d2 = x;
+                    }
+                    for (int off = 1; off < lanes; off <<= 1) {
+                        const double o1 = __shfl_xor_sync(0xffffffffu, d1, off);
+                        const double o2 = __shfl_xor_sync(0xffffffffu, d2, off);
+                        d2 = fmax(fmin(d1, o1), fmax(d2, o2));
+                        d1 = fmax(d1, o1);
+                    }
+                    const double dg = sums && d2 > -INFINITY ? d1 + d2 : d1;
+                    const int rank64 = rank_of(dg);
+                    const bool st64 = in && rank64 < a.keep;
+                    if (close) {
+                        st = st64;
+                        if (!sure || (!a.sigmoid && (BIASED || sums)) || !(fabsf(lo) < SEL_EDGE)) bad = true;
+                    }
+                }
             }
             if (!st) v[0] = -SEL_FAR;
         }
 
-        const int rounds = EXACT ? a.k : a.k + 1; // one more: the best that is left out
-#pragma unroll 1
-        for (int j = 0; j < rounds; ++j) {
-            const float top = sel_max(v[0]);
+        auto round = [&](int j) {
+            const float top = sel_max_of<LPT>(v[0]);
             const bool head = v[0] == top;
             const uint32_t all = __ballot_sync(0xffffffffu, head);
-            if (head && !(all & below)) {
-                pick[j] = make_uint2(__float_as_uint(top), (uint32_t)lane);
+            if (head && !(all & rivals)) {
+                pick[j] = make_uint2(__float_as_uint(top), (uint32_t)e0);
 #pragma unroll
                 for (int i = 0; i + 1 < D; ++i) v[i] = v[i + 1];
                 // a lane that gave all its experts has no more; one that kept eight of more might
                 v[D - 1] = EPT > D ? SEL_FAR : -SEL_FAR;
             }
-        }
+        };
+        const int rounds = EXACT ? a.k : a.k + 1; // one more: the best that is left out
+#pragma unroll 1
+        for (int j = 0; j < rounds; ++j) round(j);
         __syncwarp();
+        auto expert = [&](uint2 p) {
+            return IDS ? sel_id(__uint_as_float(p.x)) : (int)p.y + (EPT > 1 ? (int)(p.x & (uint32_t)(EPT - 1)) : 0);
+        };
+        auto apart = [&](float x, float y) { // surely in this order in 64 bits
+            return x - y > (BIASED ? tol : 0.0f) + TOL_KEY * (fabsf(x) + fabsf(y)) + SEL_TOL_ZERO;
+        };
         int mine = 0;
-        const bool on = lane < a.k;
+        const bool on = sl < a.k;
+        bool close = false;
         if (on) {
-            const uint2 p = pick[lane];
+            const uint2 p = pick[sl];
             const float key = __uint_as_float(p.x);
             if (!(fabsf(key) < SEL_EDGE)) bad = true;
-            if (!EXACT) {
-                const float after = __uint_as_float(pick[lane + 1].x);
-                if (!(key - after > (BIASED ? tol : 0.0f) + TOL_KEY * (fabsf(key) + fabsf(after)) + SEL_TOL_ZERO)) bad = true;
+            if (!EXACT && !apart(key, __uint_as_float(pick[sl + 1].x))) close = true;
+            mine = expert(p);
+        }
+        uint32_t closes = 0;
+        if (!EXACT) closes = __ballot_sync(0xffffffffu, close);
+        if (!EXACT && closes) {
+            // Winners too close to order in 32 bits: the first k + 1, if they are surely the k + 1
+            // largest, again by their keys in 64 bits
+            round(a.k + 1);
+            __syncwarp();
+            const float last = __uint_as_float(pick[a.k].x), after = __uint_as_float(pick[a.k + 1].x);
+            const bool here = (closes & (LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (seg * LPT))) != 0;
+            if (here && ((BIASED && !a.sigmoid) || !(last < SEL_EDGE && after < SEL_EDGE) ||
+                         (last > -SEL_EDGE && !apart(last, after))))
+                bad = true;
+            double *d64 = reinterpret_cast<double *>(scratch) + seg * (LPT + 2);
+            for (int j = sl; j <= a.k; j += LPT) {
+                const uint2 p = pick[j];
+                double d = -INFINITY;
+                if (fabsf(__uint_as_float(p.x)) < SEL_EDGE) {
+                    const int e = expert(p);
+                    const float l = sel_load(row + e);
+                    d = BIASED ? sel_value64(l, a.bias[e]) : (double)l;
+                }
+                d64[j] = d;
             }
-            if (IDS)
-                mine = (p.x >> 31) ? (int)(p.x & 0xffffu) : 1023 - (int)(p.x & 0xffffu);
-            else
-                mine = (int)p.y * EPT + (EPT > 1 ? (int)(p.x & (uint32_t)(EPT - 1)) : 0);
+            __syncwarp();
+            int slot = -1, id = 0, slot2 = -1, id2 = 0; // ranks of entries sl and sl + LPT
+            for (int j = sl; j <= a.k; j += LPT) {
+                const double d = d64[j];
+                const int e = expert(pick[j]);
+                int rank = 0;
+                for (int i = 0; i <= a.k; ++i)
+                    rank += d64[i] > d || (d64[i] == d && (expert(pick[i]) < e || (expert(pick[i]) == e && i < j))) ? 1 : 0;
+                if (j < LPT) {
+                    slot = rank;
+                    id = e;
+                } else {
+                    slot2 = rank;
+                    id2 = e;
+                }
+            }
+            __syncwarp();
+            if (slot >= 0) pick[slot].y = (uint32_t)id;
+            if (slot2 >= 0) pick[slot2].y = (uint32_t)id2;
+            __syncwarp();
+            if (here && on) mine = (int)pick[sl].y;
         }
         __syncwarp(); // pick and scratch are free for the next token
-        if (__any_sync(0xffffffffu, bad)) {
-            const SelExact x = sel_exact(a, row, scratch, lane);
-            mine = x.mine;
-            m = x.m;
-            sum = x.sum;
+        uint32_t again = __ballot_sync(0xffffffffu, bad);
+        while (again) { // one token at a time, the whole warp
+            const int s = LPT == 32 ? 0 : (__ffs(again) - 1) / LPT;
+            const int te = __shfl_sync(0xffffffffu, t, s * LPT);
+            const SelExact x = sel_exact(a, static_cast<const LT *>(a.logits) + (size_t)te * a.ld, scratch, lane);
+            const int xm = __shfl_sync(0xffffffffu, x.mine, sl);
+            if (seg == s) {
+                mine = xm;
+                m = x.m;
+                sum = x.sum;
+            }
             __syncwarp();
+            again &= LPT == 32 ? 0u : ~(((1u << (LPT & 31)) - 1u) << (s * LPT));
         }
 
-        // weights, once for the k selected on lanes 0 .. k - 1
+        // weights, once for the k selected on the token's first k lanes
         const float lj = on ? sel_clean(sel_load(row + mine)) : -INFINITY;
         const bool live = lj > -INFINITY;
         float u = 0.0f;
         if (a.sigmoid) {
             const float mn = fminf(lj, 0.0f);
-            const float M = a.renorm ? sel_max(live ? mn : -INFINITY) : 0.0f; // keeps tiny scores' ratios
+            const float M = a.renorm ? sel_max_of<LPT>(live ? mn : -INFINITY) : 0.0f; // keeps tiny scores' ratios
             if (live) u = __fdividef(expf(mn - M), 1.0f + expf(-fabsf(lj)));
         } else {
-            const float M = a.renorm ? sel_max(lj) : m;
+            const float M = a.renorm ? sel_max_of<LPT>(lj) : m;
             if (live) u = a.renorm ? expf(lj - M) : __fdividef(expf(lj - M), sum);
         }
         if (a.renorm) {
-            const float total = sel_sum(u);
+            const float total = sel_sum_of<LPT>(u);
             u = total > 0.0f ? __fdividef(u, total) : 0.0f;
         }
-        if (on) {
-            a.idx[(size_t)t * a.k + lane] = mine;
-            a.w[(size_t)t * a.k + lane] = a.scale * u;
+        if (on && mine_too) {
+            a.idx[(size_t)t * a.k + sl] = mine;
+            a.w[(size_t)t * a.k + sl] = a.scale * u;
         }
     }
 }
