@@ -8,7 +8,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 
 #include "dropout.cuh"
 #include "host.cuh"
@@ -43,8 +42,6 @@ moe_status check_select(const moe_select *s)
 int dtype_bytes(int32_t d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 bool aligned_to(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) % (unsigned)bytes) == 0; }
 
-std::atomic<int> g_select_wide{getenv("SELW") ? atoi(getenv("SELW")) : 2048};
-
 template <int LPT, int EPT, typename LT, bool BIASED>
 cudaError_t launch_select(const SelectArgs &a, cudaStream_t st)
 {
@@ -61,13 +58,16 @@ cudaError_t launch_select(const SelectArgs &a, cudaStream_t st)
 template <typename LT, bool BIASED> cudaError_t launch_select_wide(const SelectArgs &a, cudaStream_t st)
 {
     // Four tokens per warp where they fit (k <= 8, E <= 256, groups of whole lanes) and there are
-    // enough of them
+    // enough of them: fewer instructions a token, but longer chains a lane. Measured, a warp each
+    // against eight lanes each: E = 256 (8 groups, bias) T = 4096 7.1 / 8.2 us, 8192 9.8 / 10.3,
+    // 16384 16.1 / 14.4; E = 128 (bias) 5.2 / 6.0, 7.1 / 7.0, 10.1 / 8.9; E = 64 3.6 / 4.5, 6.1 / 4.8,
+    // 8.7 / 6.4; E = 8 T = 1024 2.2 / 2.2, 2048 2.5 / 2.3, 4096 3.0 / 2.3, 16384 5.8 / 2.9.
     int ept = 1;
     while (ept * 8 < a.E) ept *= 2;
     const int lanes = a.gsz / ept;
     const bool fits = a.k <= 8 && a.E <= 256 &&
                       (a.groups == 1 || (a.gsz % ept == 0 && (lanes & (lanes - 1)) == 0));
-    if (fits && a.T >= g_select_wide.load()) {
+    if (fits && a.T >= (a.E <= 32 ? 2048 : 8192)) {
         switch (ept) {
         case 1: return launch_select<8, 1, LT, BIASED>(a, st);
         case 2: return launch_select<8, 2, LT, BIASED>(a, st);

@@ -390,3 +390,38 @@ def test_many_rows():
         ri, rw = ref_select(sub, l[rows].float().numpy(), b.numpy())
         assert np.array_equal(idx[rows].cpu().numpy(), ri)
         assert np.all(np.abs(w[rows].cpu().numpy() - rw) <= weight_tol(sub, l[rows].float().numpy(), rw))
+
+
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+@pytest.mark.parametrize("E,k,G,keep", [(256, 8, 8, 4), (256, 8, 4, 2), (128, 5, 8, 3), (100, 8, 1, 1), (64, 1, 8, 1),
+                                        (64, 8, 2, 1), (31, 7, 1, 1), (10, 3, 5, 2), (8, 8, 1, 1), (5, 2, 1, 1)])
+def test_large_batches(E, k, G, keep, score):
+    """Batches that put several tokens on a warp: the rows of a small batch (random, tied, nearly
+    tied, masked, infinite) many times over, in another order, against the small batch's reference."""
+    U0, T = 59, 8203
+    for i, (dtype, biased, sum2, renorm) in enumerate([(torch.float32, True, 1, True), (torch.float32, False, 1, False),
+                                                       (torch.bfloat16, False, 0, True), (torch.bfloat16, True, 0, False),
+                                                       (torch.float32, False, 0, True)]):
+        l, b = draw(U0, E, 7 * E + i, dtype)
+        l[0] = -math.inf
+        l[1, 1:] = -math.inf
+        l[2, ::2] = float("nan")
+        l[3] = 0.25
+        l[4, E // 2:] = l[4, 0]
+        l[5, 1] = math.inf
+        l[6] = torch.finfo(dtype).min
+        l[7, E // 2] = 30000.0
+        l[8:12] = (l[8:12].float() * 1e-3).to(dtype)      # nearly tied
+        small = moe.Select.make(U0, E, k, score=score, n_group=G, top_group=keep, group_score=sum2, renorm=renorm)
+        big = moe.Select.make(T, E, k, score=score, n_group=G, top_group=keep, group_score=sum2, renorm=renorm)
+        bias = b if biased else None
+        ri, rw = ref_select(small, l.float().numpy(), b.numpy() if biased else None)
+        tol = weight_tol(small, l.float().numpy(), rw)
+        at = torch.randperm(T, generator=torch.Generator().manual_seed(i)) % U0
+        idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((T, k), -7.0, device="cuda")
+        moe.moe_route_select(big, l[at].cuda(), None if bias is None else bias.cuda(), idx, w)
+        gi, gw = idx.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+        a = at.numpy()
+        assert np.array_equal(gi, ri[a]), (i, np.argwhere(gi != ri[a])[:4])
+        assert np.all(np.abs(gw - rw[a]) <= tol[a])
