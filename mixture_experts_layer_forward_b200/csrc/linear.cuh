@@ -140,6 +140,39 @@ __device__ __forceinline__ void lin_tile(int w, const LinearArgs &a, int &mt, in
     nt = r / gm;
 }
 
+// One lane of a converged warp. The roles below run warp-wide, with only the copies and products
+// themselves under this predicate: their operands then stay in uniform registers. (One-lane loops
+// cost 90 to 130 cycles an instruction, which bound every tile: 0.31 us a k-block at BN = 256, 0.28
+// at BN = 64, where the products take 0.27 and 0.07.)
+__device__ __forceinline__ bool lin_elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait of a whole warp (mbar_wait_bounded for all lanes alike).
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                         int64_t timeout_ns, int *status, int where)
+{
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        const bool late = (int64_t)(globaltimer_ns() - t0) > timeout_ns;
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) {
+            if (late && *abort_flag == 0) {
+                *abort_flag = 1;
+                record_status(status, DEV_TIMEOUT, where);
+            }
+            return false;
+        }
+    }
+}
+
 // The barriers and the two pipeline roles, shared by both kernels.
 template <int BN, bool A_MN, bool B_MN> struct LinPipe {
     static constexpr int STAGES = lin::stages(BN);
@@ -164,37 +197,41 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
         }
     }
 
-    // TMA copies of k-blocks [kb0, kb1) of one tile (one thread)
+    // TMA copies of k-blocks [kb0, kb1) of one tile (one warp)
     __device__ bool produce(const CUtensorMap &tmA, const CUtensorMap &tmB, const LinearArgs &a, int mt,
                             int nt, int kb0, int kb1, volatile int *abort_flag, uint32_t &armed)
     {
         const bool gated = a.act == 0;
         const int n0 = nt * (gated ? BN / 2 : BN);
         const uint32_t bytes = (A_MN ? lin::A_TILE : a.a_rows * 128) + BN * 128;
+        const uint32_t base = smem_u32(smem);
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait_bounded(empty(s), ph ^ 1u, abort_flag, a.timeout_ns, a.status, 500)) return false;
-            const uint32_t a_dst = smem_u32(smem + s * STAGE), b_dst = a_dst + lin::A_TILE;
-            mbar_arrive_expect_tx(full(s), bytes);
+            if (!lin_wait(empty(s), ph ^ 1u, abort_flag, a.timeout_ns, a.status, 500)) return false;
+            const uint32_t a_dst = base + s * STAGE, b_dst = a_dst + lin::A_TILE;
             armed |= 1u << s;
-            if (A_MN) {
-                tma_load_2d(a_dst, &tmA, full(s), mt * lin::BM, kb * lin::BK);
-                tma_load_2d(a_dst + lin::BOX, &tmA, full(s), mt * lin::BM + 64, kb * lin::BK);
-            } else {
-                tma_load_2d(a_dst, &tmA, full(s), kb * lin::BK, mt * lin::BM);
-            }
-            if (B_MN) {
-                constexpr int NB = BN / 64;
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const int col = (gated && i >= NB / 2) ? a.up_col + n0 + (i - NB / 2) * 64 : n0 + i * 64;
-                    tma_load_2d(b_dst + i * lin::BOX, &tmB, full(s), col, kb * lin::BK);
+            if (lin_elect()) {
+                mbar_arrive_expect_tx(full(s), bytes);
+                if (A_MN) {
+                    tma_load_2d(a_dst, &tmA, full(s), mt * lin::BM, kb * lin::BK);
+                    tma_load_2d(a_dst + lin::BOX, &tmA, full(s), mt * lin::BM + 64, kb * lin::BK);
+                } else {
+                    tma_load_2d(a_dst, &tmA, full(s), kb * lin::BK, mt * lin::BM);
                 }
-            } else if (gated) { // box of BN / 2 rows
-                tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
-                tma_load_2d(b_dst + BN / 2 * 128, &tmB, full(s), kb * lin::BK, a.up_col + n0);
-            } else { // box of BN rows
-                tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
+                if (B_MN) {
+                    constexpr int NB = BN / 64;
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const int col = (gated && i >= NB / 2) ? a.up_col + n0 + (i - NB / 2) * 64 : n0 + i * 64;
+                        tma_load_2d(b_dst + i * lin::BOX, &tmB, full(s), col, kb * lin::BK);
+                    }
+                } else if (gated) { // box of BN / 2 rows
+                    tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
+                    tma_load_2d(b_dst + BN / 2 * 128, &tmB, full(s), kb * lin::BK, a.up_col + n0);
+                } else { // box of BN rows
+                    tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
+                }
             }
+            __syncwarp();
             next();
         }
         return true;
@@ -206,28 +243,32 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
         for (int i = 0; i < STAGES; ++i)
             if ((armed >> i) & 1u) {
                 volatile int never = 0;
-                mbar_wait_bounded(full(i), i < s ? ph : ph ^ 1u, &never, timeout_ns, nullptr, 0);
+                lin_wait(full(i), i < s ? ph : ph ^ 1u, &never, timeout_ns, nullptr, 0);
             }
     }
 
-    // the products of k-blocks [kb0, kb1) into d_tmem (one thread)
+    // the products of k-blocks [kb0, kb1) into d_tmem (one warp)
     __device__ bool multiply(const LinearArgs &a, uint32_t d_tmem, int kb0, int kb1,
                              volatile int *abort_flag)
     {
+        const uint32_t base = smem_u32(smem);
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait_bounded(full(s), ph, abort_flag, a.timeout_ns, a.status, 510)) return false;
+            if (!lin_wait(full(s), ph, abort_flag, a.timeout_ns, a.status, 510)) return false;
             tc_fence_after();
-            const uint32_t a_addr = smem_u32(smem + s * STAGE), b_addr = a_addr + lin::A_TILE;
+            const uint32_t a_addr = base + s * STAGE, b_addr = a_addr + lin::A_TILE;
             // K-major: rows of 128 bytes, +32 bytes per 16 k; MN-major: 64-column blocks of 64 k
             // rows, +16 rows per 16 k
             const uint64_t ad = A_MN ? sw128_desc(a_addr, lin::BOX, 1024) : sw128_desc(a_addr, 16, 1024);
             const uint64_t bd = B_MN ? sw128_desc(b_addr, lin::BOX, 1024) : sw128_desc(b_addr, 16, 1024);
+            if (lin_elect()) {
 #pragma unroll
-            for (int k = 0; k < lin::BK / 16; ++k)
-                umma_bf16(d_tmem, ad + (uint64_t)((A_MN ? k * 2048 : k * 32) >> 4),
-                          bd + (uint64_t)((B_MN ? k * 2048 : k * 32) >> 4), IDESC,
-                          (kb != kb0 || k != 0) ? 1u : 0u);
-            umma_commit(empty(s));
+                for (int k = 0; k < lin::BK / 16; ++k)
+                    umma_bf16(d_tmem, ad + (uint64_t)((A_MN ? k * 2048 : k * 32) >> 4),
+                              bd + (uint64_t)((B_MN ? k * 2048 : k * 32) >> 4), IDESC,
+                              (kb != kb0 || k != 0) ? 1u : 0u);
+                umma_commit(empty(s));
+            }
+            __syncwarp();
             next();
         }
         return true;
@@ -279,31 +320,27 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int total = a.m_tiles * a.n_tiles;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t armed = 0;
-            for (int w = blockIdx.x; w < total; w += gridDim.x) {
-                int mt, nt;
-                lin_tile(w, a, mt, nt);
-                if (!p.produce(tmA, tmB, a, mt, nt, 0, a.k_blocks, abort_flag, armed)) break;
-            }
-            p.drain(armed, a.timeout_ns);
+        uint32_t armed = 0;
+        for (int w = blockIdx.x; w < total; w += gridDim.x) {
+            int mt, nt;
+            lin_tile(w, a, mt, nt);
+            if (!p.produce(tmA, tmB, a, mt, nt, 0, a.k_blocks, abort_flag, armed)) break;
         }
+        p.drain(armed, a.timeout_ns);
     } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0;
-            for (int w = blockIdx.x; w < total; w += gridDim.x, ++it) {
-                const int acc = it & 1;
-                if (!mbar_wait_bounded(p.tempty(acc), ((it >> 1) & 1) ^ 1, abort_flag, a.timeout_ns,
-                                       a.status, 520))
-                    break;
-                tc_fence_after();
-                if (!p.multiply(a, tmem + acc * BN, 0, a.k_blocks, abort_flag)) break;
-                umma_commit(p.tfull(acc));
-            }
-            umma_commit(p.done()); // every product is finished before TMEM is released
-            volatile int never = 0;
-            mbar_wait_bounded(p.done(), 0, &never, a.timeout_ns, a.status, 530);
+        int it = 0;
+        for (int w = blockIdx.x; w < total; w += gridDim.x, ++it) {
+            const int acc = it & 1;
+            if (!lin_wait(p.tempty(acc), ((it >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status, 520)) break;
+            tc_fence_after();
+            if (!p.multiply(a, tmem + acc * BN, 0, a.k_blocks, abort_flag)) break;
+            if (lin_elect()) umma_commit(p.tfull(acc));
+            __syncwarp();
         }
+        if (lin_elect()) umma_commit(p.done()); // every product is finished before TMEM is released
+        __syncwarp();
+        volatile int never = 0;
+        lin_wait(p.done(), 0, &never, a.timeout_ns, a.status, 530);
     } else {
         const int q = warp & 3, half = warp >= 6 ? 1 : 0;
         const bool gated = a.act == 0;
@@ -415,16 +452,13 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     float *park = reinterpret_cast<float *>(p.smem);
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t armed = 0;
-            p.produce(tmA, tmB, a, mt, nt, kb0, kb1, abort_flag, armed);
-            p.drain(armed, a.timeout_ns);
-        }
+        uint32_t armed = 0;
+        p.produce(tmA, tmB, a, mt, nt, kb0, kb1, abort_flag, armed);
+        p.drain(armed, a.timeout_ns);
     } else if (warp == 1) {
-        if (lane == 0) {
-            p.multiply(a, tmem, kb0, kb1, abort_flag);
-            umma_commit(p.tfull(0)); // every product issued is finished
-        }
+        p.multiply(a, tmem, kb0, kb1, abort_flag);
+        if (lin_elect()) umma_commit(p.tfull(0)); // every product issued is finished
+        __syncwarp();
     } else {
         const int q = warp & 3, half = warp >= 6 ? 1 : 0;
         // the products issued finish on their own: this wait ends with them, or runs out
