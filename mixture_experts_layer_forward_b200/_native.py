@@ -88,7 +88,8 @@ def _dtype_code(dtype):
 
 
 class Select(ctypes.Structure):
-    """moe_select: routing by scores. The logits' type is taken from the tensors of each call."""
+    """moe_select: routing by scores. The type and row stride of the logits are taken from each
+    call's tensor (dtype is the type that needs no copy of the structure)."""
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("score", ctypes.c_int32), ("n_group", ctypes.c_int32),
                 ("top_group", ctypes.c_int32), ("group_score", ctypes.c_int32),
@@ -97,9 +98,9 @@ class Select(ctypes.Structure):
 
     @classmethod
     def make(cls, T, E, top_k, score=SCORE_SIGMOID, n_group=1, top_group=1, group_score=GROUP_MAX,
-             renorm=True, scale=1.0):
-        return cls(T, E, top_k, score, n_group, top_group, group_score, 1 if renorm else 0, 0,
-                   scale, 0)
+             renorm=True, scale=1.0, dtype=torch.float32):
+        return cls(T, E, top_k, score, n_group, top_group, group_score, 1 if renorm else 0,
+                   _dtype_code(dtype), scale, 0)
 
 
 class Linear(ctypes.Structure):
@@ -131,6 +132,8 @@ def library_path() -> Path:
 def library() -> ctypes.CDLL:
     """Load libmoe_b200.so. Raises if it has not been built: there is no fallback path."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -651,87 +654,113 @@ def moe_ep_layer_forward(ranks, stream=None):
 # operators around the layer: routing by scores, the dense product, dropout with the residual
 # ---------------------------------------------------------------------------------------
 
-class _Call:
-    """Checks of one call's tensors: type, shape, rows dense inside, all on one CUDA device that
-    is the current one (the launch goes to the current device's stream)."""
-    __slots__ = ("device",)
+_Tensor = torch.Tensor
 
-    def __init__(self):
-        self.device = None
 
-    def rows(self, t, dtype, shape, name, strided=False):
-        """Address and row stride of a tensor (None: 0, 0). strided: rows may be apart."""
-        if t is None:
-            return None, 0
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        device = t.get_device()
-        if device < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if self.device is None:
-            self.device = device
-            if device != torch.cuda.current_device():
-                raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
-        elif device != self.device:
-            raise ValueError(f"{name} is on cuda:{device}, other tensors on cuda:{self.device}")
+def _refuse(t, dtype, shape, name, device, strided=False):
+    """Raise for the first thing that is wrong with a tensor argument."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other arguments on cuda:{device}")
+    raise ValueError(f"{name} must be contiguous" + (" within its rows" if strided else ""))
+
+
+def _device(t, name):
+    """The device of a call's first tensor, which must be the current one (the launch goes to a
+    stream of the current device)."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    device = t.get_device()
+    if device < 0:
+        return device                      # refused with its name by the checks that follow
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{device}, which is not the current device")
+    return device
+
+
+def _dense(t, dtype, shape, name, device):
+    """Address of a contiguous tensor of this type, shape and device; None for None."""
+    if t is None:
+        return None
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and device >= 0
+            and t.get_device() == device and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, dtype, shape, name, device)
+
+
+def _rows(t, dtype, shape, name, device):
+    """Address and row stride (0: contiguous) of a matrix whose rows may lie apart."""
+    if t is None:
+        return None, 0
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and device >= 0
+            and t.get_device() == device):
         if t.is_contiguous():
             return t.data_ptr(), 0
-        if not strided or t.stride(-1) != 1 or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{name} must be contiguous" + (" within its rows" if strided else ""))
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
-
-    def stream(self, stream):
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-        if isinstance(stream, torch.cuda.Stream):
-            if self.device is not None and stream.device_index != self.device:
-                raise ValueError("stream is not on the tensors' device")
-            return stream.cuda_stream
-        return int(stream)
+        if t.stride(1) == 1 and (shape[0] <= 1 or t.stride(0) >= shape[1]):
+            return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+    _refuse(t, dtype, shape, name, device, strided=True)
 
 
-def _route_dtype(logits):
-    if not isinstance(logits, torch.Tensor):
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != device:
+            raise ValueError("stream is not on the tensors' device")
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _select_for(s, logits, ld):
+    """s with this call's type and row stride (s itself where it has them)."""
+    if not isinstance(logits, _Tensor):
         raise TypeError("logits must be a torch.Tensor")
-    return _dtype_code(logits.dtype)
-
-
-def _select_with(s, dtype, ld):
-    return Select(s.T, s.E, s.top_k, s.score, s.n_group, s.top_group, s.group_score, s.renorm, dtype,
-                  s.scale, ld)
+    code = _dtype_code(logits.dtype)
+    if s.dtype == code and s.ld == ld:
+        return s
+    c = Select.from_buffer_copy(s)
+    c.dtype, c.ld = code, ld
+    return c
 
 
 def moe_route_select(s: Select, logits, bias, topk_idx, topk_w, n_rows=None, stream=None):
     """Routing by scores: logits [T, E] float32 or bfloat16 (rows may be apart), bias [E] float32
     or None -> topk_idx [T, k] int32, topk_w [T, k] float32. n_rows: a CUDA int32 tensor; rows from
     n_rows[0] on are left as they are."""
-    c = _Call()
-    dt, i32, f32 = _route_dtype(logits), torch.int32, torch.float32
-    lp, ld = c.rows(logits, logits.dtype, (s.T, s.E), "logits", strided=True)
+    d = _device(logits, "logits")
+    T, E, i32, f32 = s.T, s.E, torch.int32, torch.float32
+    out = (T, s.top_k)
+    _dtype_code(logits.dtype)
+    lp, ld = _rows(logits, logits.dtype, (T, E), "logits", d)
     rc = library().moe_route_select(
-        _select_with(s, dt, ld), lp, c.rows(bias, f32, (s.E,), "bias")[0],
-        c.rows(topk_idx, i32, (s.T, s.top_k), "topk_idx")[0],
-        c.rows(topk_w, f32, (s.T, s.top_k), "topk_w")[0],
-        c.rows(n_rows, i32, (1,), "n_rows")[0], c.stream(stream))
-    _check("moe_route_select", rc)
+        _select_for(s, logits, ld), lp, _dense(bias, f32, (E,), "bias", d),
+        _dense(topk_idx, i32, out, "topk_idx", d), _dense(topk_w, f32, out, "topk_w", d),
+        _dense(n_rows, i32, (1,), "n_rows", d), _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_route_select", rc)
 
 
 def moe_route_select_backward(s: Select, logits, topk_idx, dtopk_w, dlogits, n_rows=None,
                               stream=None):
     """dlogits [T, E] (the logits' type) from dtopk_w [T, k] float32, the selection held fixed."""
-    c = _Call()
-    dt, i32, f32 = _route_dtype(logits), torch.int32, torch.float32
-    lp, ld = c.rows(logits, logits.dtype, (s.T, s.E), "logits", strided=True)
+    d = _device(logits, "logits")
+    T, E, i32, f32 = s.T, s.E, torch.int32, torch.float32
+    _dtype_code(logits.dtype)
+    lp, ld = _rows(logits, logits.dtype, (T, E), "logits", d)
     rc = library().moe_route_select_backward(
-        _select_with(s, dt, ld), lp, c.rows(topk_idx, i32, (s.T, s.top_k), "topk_idx")[0],
-        c.rows(dtopk_w, f32, (s.T, s.top_k), "dtopk_w")[0],
-        c.rows(dlogits, logits.dtype, (s.T, s.E), "dlogits")[0],
-        c.rows(n_rows, i32, (1,), "n_rows")[0], c.stream(stream))
-    _check("moe_route_select_backward", rc)
+        _select_for(s, logits, ld), lp, _dense(topk_idx, i32, (T, s.top_k), "topk_idx", d),
+        _dense(dtopk_w, f32, (T, s.top_k), "dtopk_w", d),
+        _dense(dlogits, logits.dtype, (T, E), "dlogits", d),
+        _dense(n_rows, i32, (1,), "n_rows", d), _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_route_select_backward", rc)
 
 
 def moe_linear_workspace_size(p: Linear) -> int:
@@ -744,46 +773,56 @@ def moe_linear_backward_workspace_size(p: Linear) -> int:
     return int(library().moe_linear_backward_workspace_size(p))
 
 
+def _linear_for(p, ldx, ldw, ldr, ldy, ldz):
+    """p with this call's row strides (p itself where every row is dense)."""
+    if not (ldx or ldw or ldr or ldy or ldz):
+        if not (p.ldx or p.ldw or p.ldr or p.ldy or p.ldz):
+            return p
+    c = Linear.from_buffer_copy(p)
+    c.ldx, c.ldw, c.ldr, c.ldy, c.ldz = ldx, ldw, ldr, ldy, ldz
+    return c
+
+
 def _out_dtype(p):
     return torch.float32 if p.out_dtype == 1 else torch.bfloat16
-
-
-def _w_shape(p):
-    return (p.K, p.cols) if p.w_layout == W_KN else (p.cols, p.K)
 
 
 def moe_linear_forward(p: Linear, x, W, bias, residual, y, ws, z=None, stream=None):
     """y = act(x W + bias) + residual; z (bfloat16, optional) receives the pre-activation. x, W,
     residual, y and z may have rows apart (16-byte aligned); bias float32 [p.cols] or None."""
-    c, bf = _Call(), torch.bfloat16
-    xp, ldx = c.rows(x, bf, (p.M, p.K), "x", strided=True)
-    wp, ldw = c.rows(W, bf, _w_shape(p), "W", strided=True)
-    rp, ldr = c.rows(residual, bf, (p.M, p.N), "residual", strided=True)
-    yp, ldy = c.rows(y, _out_dtype(p), (p.M, p.N), "y", strided=True)
-    zp, ldz = c.rows(z, bf, (p.M, p.cols), "z", strided=True)
+    d, bf = _device(x, "x"), torch.bfloat16
+    M, N, K, cols = p.M, p.N, p.K, p.cols
+    xp, ldx = _rows(x, bf, (M, K), "x", d)
+    wp, ldw = _rows(W, bf, (K, cols) if p.w_layout == W_KN else (cols, K), "W", d)
+    rp, ldr = _rows(residual, bf, (M, N), "residual", d)
+    yp, ldy = _rows(y, _out_dtype(p), (M, N), "y", d)
+    zp, ldz = _rows(z, bf, (M, cols), "z", d)
     n = ws.numel()
     rc = library().moe_linear_forward(
-        Linear(p.M, p.N, p.K, p.act, p.w_layout, p.out_dtype, ldx, ldw, ldr, ldy, ldz), xp, wp,
-        c.rows(bias, torch.float32, (p.cols,), "bias")[0], rp, yp, zp,
-        c.rows(ws, torch.uint8, (n,), "ws")[0], n, c.stream(stream))
-    _check("moe_linear_forward", rc)
+        _linear_for(p, ldx, ldw, ldr, ldy, ldz), xp, wp,
+        _dense(bias, torch.float32, (cols,), "bias", d), rp, yp, zp,
+        _dense(ws, torch.uint8, (n,), "ws", d), n, _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_linear_forward", rc)
 
 
 def moe_linear_backward(p: Linear, x, W, z, dy, dx, dW, dbias, ws, stream=None):
     """dx [M, K], dW (W's layout) bfloat16 and dbias [p.cols] float32 (each may be None: not
     wanted) from dy [M, N] and the z that moe_linear_forward wrote (None for ACT_IDENTITY)."""
-    c, bf = _Call(), torch.bfloat16
-    xp, ldx = c.rows(x, bf, (p.M, p.K), "x", strided=True)
-    wp, ldw = c.rows(W, bf, _w_shape(p), "W", strided=True)
-    zp, ldz = c.rows(z, bf, (p.M, p.cols), "z", strided=True)
-    dyp, ldy = c.rows(dy, _out_dtype(p), (p.M, p.N), "dy", strided=True)
+    d, bf = _device(dy, "dy"), torch.bfloat16
+    M, N, K, cols = p.M, p.N, p.K, p.cols
+    w_shape = (K, cols) if p.w_layout == W_KN else (cols, K)
+    xp, ldx = _rows(x, bf, (M, K), "x", d)
+    wp, ldw = _rows(W, bf, w_shape, "W", d)
+    zp, ldz = _rows(z, bf, (M, cols), "z", d)
+    dyp, ldy = _rows(dy, _out_dtype(p), (M, N), "dy", d)
     n = ws.numel()
     rc = library().moe_linear_backward(
-        Linear(p.M, p.N, p.K, p.act, p.w_layout, p.out_dtype, ldx, ldw, 0, ldy, ldz), xp, wp, zp, dyp,
-        c.rows(dx, bf, (p.M, p.K), "dx")[0], c.rows(dW, bf, _w_shape(p), "dW")[0],
-        c.rows(dbias, torch.float32, (p.cols,), "dbias")[0], c.rows(ws, torch.uint8, (n,), "ws")[0], n,
-        c.stream(stream))
-    _check("moe_linear_backward", rc)
+        _linear_for(p, ldx, ldw, 0, ldy, ldz), xp, wp, zp, dyp, _dense(dx, bf, (M, K), "dx", d),
+        _dense(dW, bf, w_shape, "dW", d), _dense(dbias, torch.float32, (cols,), "dbias", d),
+        _dense(ws, torch.uint8, (n,), "ws", d), n, _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_linear_backward", rc)
 
 
 def moe_set_linear_plan(tile_n: int, splits: int) -> None:
@@ -801,60 +840,66 @@ def _drop(prob):
 
 def moe_dropout_add(x, residual, y, prob: float, rng, stream=None):
     """y = residual + dropout(x): x, residual (or None), y of one shape and type (bfloat16 or
-    float32); prob is rounded to a multiple of 2^-16; rng: CUDA int64 tensor (seed, offset); the call uses ceil(x.numel() / 8) counters of
-    it. The mask is never stored: moe_dropout_add_backward forms it again from the same rng."""
-    c, dt = _Call(), _route_dtype(x)
+    float32); prob is rounded to a multiple of 2^-16; rng: CUDA int64 tensor (seed, offset); the call
+    uses ceil(x.numel() / 8) counters of it. The mask is never stored: moe_dropout_add_backward
+    forms it again from the same rng."""
+    d, drop = _device(x, "x"), _drop(prob)
+    dt, shape = x.dtype, x.shape
     rc = library().moe_dropout_add(
-        x.numel(), dt, _drop(prob), c.rows(rng, torch.int64, (2,), "rng")[0],
-        c.rows(x, x.dtype, x.shape, "x")[0], c.rows(residual, x.dtype, x.shape, "residual")[0],
-        c.rows(y, x.dtype, x.shape, "y")[0], c.stream(stream))
-    _check("moe_dropout_add", rc)
+        x.numel(), _dtype_code(dt), drop, _dense(rng, torch.int64, (2,), "rng", d),
+        _dense(x, dt, shape, "x", d), _dense(residual, dt, shape, "residual", d),
+        _dense(y, dt, shape, "y", d), _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_dropout_add", rc)
 
 
 def moe_dropout_add_backward(dy, dx, prob: float, rng, stream=None):
     """dx = dropout's gradient of dy, with the mask of the forward call that used these rng values
     (the residual's gradient is dy)."""
-    c, dt = _Call(), _route_dtype(dy)
+    d, drop = _device(dy, "dy"), _drop(prob)
+    dt, shape = dy.dtype, dy.shape
     rc = library().moe_dropout_add_backward(
-        dy.numel(), dt, _drop(prob), c.rows(rng, torch.int64, (2,), "rng")[0],
-        c.rows(dy, dy.dtype, dy.shape, "dy")[0], c.rows(dx, dy.dtype, dy.shape, "dx")[0],
-        c.stream(stream))
-    _check("moe_dropout_add_backward", rc)
+        dy.numel(), _dtype_code(dt), drop, _dense(rng, torch.int64, (2,), "rng", d),
+        _dense(dy, dt, shape, "dy", d), _dense(dx, dt, shape, "dx", d), _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_dropout_add_backward", rc)
 
 
 def moe_forward_routed(p, x, topk_idx, topk_w, W1, W2, out, ws, shared=None, stream=None):
     """The layer with a supplied routing (topk_idx [T, k] int32, topk_w [T, k] float32, for
     instance moe_route_select's). shared: None or (W1s, W2s, w_sg), as moe_forward_shared takes
     them (workspace moe_workspace_size_shared)."""
-    c, bf = _Call(), torch.bfloat16
+    d, bf = _device(x, "x"), torch.bfloat16
     w1c = 2 * p.F if p.act == ACT_SWIGLU else p.F
+    xs, ks, n = (p.T, p.H), (p.T, p.top_k), ws.numel()
     sh = None
     if shared is not None:
         W1s, W2s, w_sg = shared
         fs = int(W2s.shape[0])
-        sh = SharedExpert(fs, c.rows(W1s, bf, (p.H, 2 * fs), "W1s")[0],
-                          c.rows(W2s, bf, (fs, p.H), "W2s")[0], c.rows(w_sg, bf, (p.H,), "w_sg")[0])
-    n = ws.numel()
+        sh = SharedExpert(fs, _dense(W1s, bf, (p.H, 2 * fs), "W1s", d),
+                          _dense(W2s, bf, (fs, p.H), "W2s", d), _dense(w_sg, bf, (p.H,), "w_sg", d))
     rc = library().moe_forward_routed(
-        p, c.rows(x, bf, (p.T, p.H), "x")[0], c.rows(topk_idx, torch.int32, (p.T, p.top_k), "topk_idx")[0],
-        c.rows(topk_w, torch.float32, (p.T, p.top_k), "topk_w")[0],
-        c.rows(W1, bf, (p.E, p.H, w1c), "W1")[0], c.rows(W2, bf, (p.E, p.F, p.H), "W2")[0], sh,
-        c.rows(out, bf, (p.T, p.H), "out")[0], c.rows(ws, torch.uint8, (n,), "ws")[0], n,
-        c.stream(stream))
-    _check("moe_forward_routed", rc)
+        p, _dense(x, bf, xs, "x", d), _dense(topk_idx, torch.int32, ks, "topk_idx", d),
+        _dense(topk_w, torch.float32, ks, "topk_w", d), _dense(W1, bf, (p.E, p.H, w1c), "W1", d),
+        _dense(W2, bf, (p.E, p.F, p.H), "W2", d), sh, _dense(out, bf, xs, "out", d),
+        _dense(ws, torch.uint8, (n,), "ws", d), n, _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_forward_routed", rc)
 
 
 def moe_backward_routed(p, x, topk_idx, topk_w, W1, W2, dout, dx, dtopk_w, dW1, dW2, ws, stream=None):
     """Gradients of moe_forward_routed (no shared expert): dx, dW1, dW2 bfloat16 and dtopk_w [T, k]
     float32, for moe_route_select_backward. Workspace: moe_backward_workspace_size."""
-    c, bf, f32 = _Call(), torch.bfloat16, torch.float32
+    d, bf, f32 = _device(x, "x"), torch.bfloat16, torch.float32
     w1c = 2 * p.F if p.act == ACT_SWIGLU else p.F
     w1s, w2s, xs, ks = (p.E, p.H, w1c), (p.E, p.F, p.H), (p.T, p.H), (p.T, p.top_k)
     n = ws.numel()
     rc = library().moe_backward_routed(
-        p, c.rows(x, bf, xs, "x")[0], c.rows(topk_idx, torch.int32, ks, "topk_idx")[0],
-        c.rows(topk_w, f32, ks, "topk_w")[0], c.rows(W1, bf, w1s, "W1")[0],
-        c.rows(W2, bf, w2s, "W2")[0], c.rows(dout, bf, xs, "dout")[0], c.rows(dx, bf, xs, "dx")[0],
-        c.rows(dtopk_w, f32, ks, "dtopk_w")[0], c.rows(dW1, bf, w1s, "dW1")[0],
-        c.rows(dW2, bf, w2s, "dW2")[0], c.rows(ws, torch.uint8, (n,), "ws")[0], n, c.stream(stream))
-    _check("moe_backward_routed", rc)
+        p, _dense(x, bf, xs, "x", d), _dense(topk_idx, torch.int32, ks, "topk_idx", d),
+        _dense(topk_w, f32, ks, "topk_w", d), _dense(W1, bf, w1s, "W1", d),
+        _dense(W2, bf, w2s, "W2", d), _dense(dout, bf, xs, "dout", d), _dense(dx, bf, xs, "dx", d),
+        _dense(dtopk_w, f32, ks, "dtopk_w", d), _dense(dW1, bf, w1s, "dW1", d),
+        _dense(dW2, bf, w2s, "dW2", d), _dense(ws, torch.uint8, (n,), "ws", d), n,
+        _raw_stream(stream, d))
+    if rc:
+        raise MoeError("moe_backward_routed", rc)
