@@ -12,7 +12,7 @@
 // Edges need no padding: copies past a tensor's end read zeros, and the epilogue stores only
 // rows < M and columns < N.
 //
-// A block has ten warps: one issues TMA copies into a ring of 128-byte-swizzled stages (64
+// A block has ten warps: one issues TMA copies into a ring of 128-byte-swizzled stages (64 or 128
 // values of k each), one issues tcgen05.mma (M = 128, N = BN, fp32 accumulators in TMEM), eight
 // run the epilogue (each pair of warps shares 32 rows and splits the columns).
 //   linear_kernel        persistent, one block per SM, two accumulators, so that a tile's
@@ -33,15 +33,22 @@ namespace moe {
 
 namespace lin {
 constexpr int BM = 128;
-constexpr int BK = 64;
-constexpr int A_TILE = BM * BK * 2; // 16 KB
-constexpr int BOX = 64 * BK * 2;    // 8 KB: 64 columns x 64 k rows of an MN-major operand
-constexpr int THREADS = 320;        // TMA warp, MMA warp, 8 epilogue warps
+constexpr int A_BOX = BM * 64 * 2; // 16 KB: 128 rows x 64 k, or two boxes of 64 columns x 64 k rows
+constexpr int BOX = 64 * 64 * 2;   // 8 KB: 64 columns x 64 k rows of an MN-major operand
+constexpr int THREADS = 320;       // TMA warp, MMA warp, 8 epilogue warps
 constexpr int EPI_THREADS = 256;
-__host__ __device__ constexpr int stage_bytes(int bn) { return A_TILE + bn * BK * 2; }
-__host__ __device__ constexpr int stages(int bn) { return 196608 / stage_bytes(bn); } // 4, 6, 8 for BN = 256, 128, 64
+// 64-value blocks of k in a stage: a narrow tile's products are shorter than the barrier's round trip,
+// so its stages hold two
+__host__ __device__ constexpr int sub(int bn) { return bn == 256 ? 1 : 2; }
+__host__ __device__ constexpr int bk(int bn) { return 64 * sub(bn); }
+__host__ __device__ constexpr int stage_bytes(int bn) { return sub(bn) * (A_BOX + bn * 128); }
+__host__ __device__ constexpr int stages(int bn) { return 196608 / stage_bytes(bn); } // 4, 3, 4 for BN = 256, 128, 64
 __host__ __device__ constexpr int num_bars(int bn) { return 2 * stages(bn) + 5; }
 __host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages(bn) * stage_bytes(bn) + num_bars(bn) * 8 + 16; }
+// fp32 outputs: k values summed in one accumulator before its values are added up in registers (the
+// tensor core adds to an accumulator by truncation, about 2^-26 of it a step of 16: 3.8e-6 over
+// K = 7168, 5e-7 over 512)
+constexpr int PROMOTE_K = 512;
 } // namespace lin
 
 struct LinearArgs {
@@ -88,10 +95,17 @@ __device__ __forceinline__ float lin_gelu(float z)
     return __fdividef(z, 1.0f + __expf(-c2 * (z + 0.044715f * z * z * z)));
 }
 
+// The residual of eight columns (zeros outside the output).
+__device__ __forceinline__ uint4 lin_res8(const LinearArgs &a, int row, int col)
+{
+    if (a.res == nullptr || row >= a.M || col >= a.N) return make_uint4(0u, 0u, 0u, 0u);
+    return *reinterpret_cast<const uint4 *>(a.res + (size_t)row * a.ldr + col);
+}
+
 // Eight consecutive output columns of one row (col % 8 == 0, N % 8 == 0): v the accumulators
-// (SwiGLU: v the gate's, u the up's).
+// (SwiGLU: v the gate's, u the up's), r the residual, loaded ahead.
 __device__ __forceinline__ void lin_finish8(const LinearArgs &a, int row, int col, float (&v)[8],
-                                            float (&u)[8])
+                                            float (&u)[8], const uint4 &r)
 {
     if (row >= a.M || col >= a.N) return;
     if (a.bias != nullptr) lin_bias8(a.bias + col, v);
@@ -116,7 +130,6 @@ __device__ __forceinline__ void lin_finish8(const LinearArgs &a, int row, int co
         }
     }
     if (a.res != nullptr) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(a.res + (size_t)row * a.ldr + col);
         v[0] += bf16_lo(r.x); v[1] += bf16_hi(r.x); v[2] += bf16_lo(r.y); v[3] += bf16_hi(r.y);
         v[4] += bf16_lo(r.z); v[5] += bf16_hi(r.z); v[6] += bf16_lo(r.w); v[7] += bf16_hi(r.w);
     }
@@ -173,10 +186,18 @@ __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// Programmatic launch order: the next call's blocks may be set up from here on; and what earlier
+// launches wrote is visible after the wait (every thread waits, so a call never ends before the
+// ones in front of it).
+__device__ __forceinline__ void lin_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void lin_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The barriers and the two pipeline roles, shared by both kernels.
 template <int BN, bool A_MN, bool B_MN> struct LinPipe {
     static constexpr int STAGES = lin::stages(BN);
     static constexpr int STAGE = lin::stage_bytes(BN);
+    static constexpr int SUB = lin::sub(BN);
+    static constexpr int SUB_BYTES = lin::A_BOX + BN * 128; // one 64-value block of k: A, then B
     static constexpr uint32_t IDESC =
         idesc_bf16_f32(lin::BM, BN, B_MN) | ((A_MN ? 1u : 0u) << 15);
     uint8_t *smem;
@@ -196,6 +217,19 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
             ph ^= 1u;
         }
     }
+    __device__ void init_bars(bool two_sided)
+    {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull(i), 1);
+            if (two_sided) mbar_init(tempty(i), 8);
+        }
+        mbar_init(done(), 1);
+        fence_mbar_init();
+    }
 
     // TMA copies of k-blocks [kb0, kb1) of one tile (one warp)
     __device__ bool produce(const CUtensorMap &tmA, const CUtensorMap &tmB, const LinearArgs &a, int mt,
@@ -203,32 +237,36 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
     {
         const bool gated = a.act == 0;
         const int n0 = nt * (gated ? BN / 2 : BN);
-        const uint32_t bytes = (A_MN ? lin::A_TILE : a.a_rows * 128) + BN * 128;
+        const uint32_t bytes = SUB * ((A_MN ? lin::A_BOX : a.a_rows * 128) + BN * 128);
         const uint32_t base = smem_u32(smem);
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!lin_wait(empty(s), ph ^ 1u, abort_flag, a.timeout_ns, a.status, 500)) return false;
-            const uint32_t a_dst = base + s * STAGE, b_dst = a_dst + lin::A_TILE;
             armed |= 1u << s;
             if (lin_elect()) {
                 mbar_arrive_expect_tx(full(s), bytes);
-                if (A_MN) {
-                    tma_load_2d(a_dst, &tmA, full(s), mt * lin::BM, kb * lin::BK);
-                    tma_load_2d(a_dst + lin::BOX, &tmA, full(s), mt * lin::BM + 64, kb * lin::BK);
-                } else {
-                    tma_load_2d(a_dst, &tmA, full(s), kb * lin::BK, mt * lin::BM);
-                }
-                if (B_MN) {
-                    constexpr int NB = BN / 64;
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const int col = (gated && i >= NB / 2) ? a.up_col + n0 + (i - NB / 2) * 64 : n0 + i * 64;
-                        tma_load_2d(b_dst + i * lin::BOX, &tmB, full(s), col, kb * lin::BK);
+                for (int j = 0; j < SUB; ++j) {
+                    const uint32_t a_dst = base + s * STAGE + j * SUB_BYTES, b_dst = a_dst + lin::A_BOX;
+                    const int k = (kb * SUB + j) * 64;
+                    if (A_MN) {
+                        tma_load_2d(a_dst, &tmA, full(s), mt * lin::BM, k);
+                        tma_load_2d(a_dst + lin::BOX, &tmA, full(s), mt * lin::BM + 64, k);
+                    } else {
+                        tma_load_2d(a_dst, &tmA, full(s), k, mt * lin::BM);
                     }
-                } else if (gated) { // box of BN / 2 rows
-                    tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
-                    tma_load_2d(b_dst + BN / 2 * 128, &tmB, full(s), kb * lin::BK, a.up_col + n0);
-                } else { // box of BN rows
-                    tma_load_2d(b_dst, &tmB, full(s), kb * lin::BK, n0);
+                    if (B_MN) {
+                        constexpr int NB = BN / 64;
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const int col = (gated && i >= NB / 2) ? a.up_col + n0 + (i - NB / 2) * 64 : n0 + i * 64;
+                            tma_load_2d(b_dst + i * lin::BOX, &tmB, full(s), col, k);
+                        }
+                    } else if (gated) { // box of BN / 2 rows
+                        tma_load_2d(b_dst, &tmB, full(s), k, n0);
+                        tma_load_2d(b_dst + BN / 2 * 128, &tmB, full(s), k, a.up_col + n0);
+                    } else { // box of BN rows
+                        tma_load_2d(b_dst, &tmB, full(s), k, n0);
+                    }
                 }
             }
             __syncwarp();
@@ -255,17 +293,20 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!lin_wait(full(s), ph, abort_flag, a.timeout_ns, a.status, 510)) return false;
             tc_fence_after();
-            const uint32_t a_addr = base + s * STAGE, b_addr = a_addr + lin::A_TILE;
-            // K-major: rows of 128 bytes, +32 bytes per 16 k; MN-major: 64-column blocks of 64 k
-            // rows, +16 rows per 16 k
-            const uint64_t ad = A_MN ? sw128_desc(a_addr, lin::BOX, 1024) : sw128_desc(a_addr, 16, 1024);
-            const uint64_t bd = B_MN ? sw128_desc(b_addr, lin::BOX, 1024) : sw128_desc(b_addr, 16, 1024);
             if (lin_elect()) {
 #pragma unroll
-                for (int k = 0; k < lin::BK / 16; ++k)
-                    umma_bf16(d_tmem, ad + (uint64_t)((A_MN ? k * 2048 : k * 32) >> 4),
-                              bd + (uint64_t)((B_MN ? k * 2048 : k * 32) >> 4), IDESC,
-                              (kb != kb0 || k != 0) ? 1u : 0u);
+                for (int j = 0; j < SUB; ++j) {
+                    const uint32_t a_addr = base + s * STAGE + j * SUB_BYTES, b_addr = a_addr + lin::A_BOX;
+                    // K-major: rows of 128 bytes, +32 bytes per 16 k; MN-major: 64-column blocks of
+                    // 64 k rows, +16 rows per 16 k
+                    const uint64_t ad = A_MN ? sw128_desc(a_addr, lin::BOX, 1024) : sw128_desc(a_addr, 16, 1024);
+                    const uint64_t bd = B_MN ? sw128_desc(b_addr, lin::BOX, 1024) : sw128_desc(b_addr, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(d_tmem, ad + (uint64_t)((A_MN ? k * 2048 : k * 32) >> 4),
+                                  bd + (uint64_t)((B_MN ? k * 2048 : k * 32) >> 4), IDESC,
+                                  (kb != kb0 || (j | k) != 0) ? 1u : 0u);
+                }
                 umma_commit(empty(s));
             }
             __syncwarp();
@@ -273,9 +314,36 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
         }
         return true;
     }
+
+    // the products of k-blocks [kb0, kb1) in runs of `run`, each into the accumulator of its turn
+    __device__ bool multiply_runs(const LinearArgs &a, uint32_t tmem, int kb0, int kb1, int run, int &it,
+                                  volatile int *abort_flag)
+    {
+        for (int kb = kb0; kb < kb1; kb += run, ++it) {
+            const int acc = it & 1;
+            if (!lin_wait(tempty(acc), ((it >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status, 520)) return false;
+            tc_fence_after();
+            if (!multiply(a, tmem + acc * BN, kb, min(kb + run, kb1), abort_flag)) return false;
+            if (lin_elect()) umma_commit(tfull(acc));
+            __syncwarp();
+        }
+        return true;
+    }
 };
 
-template <int BN, bool A_MN, bool B_MN>
+// One warp's part of a finished run: 32 rows (TMEM lanes q * 32 ..), columns [c * 32, c * 32 + 32) of the
+// accumulator, added to sum.
+__device__ __forceinline__ void lin_add32(uint32_t t_row, int c, float *sum)
+{
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(t_row + c * 32, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(r[i]);
+}
+
+// PROMOTE: runs of lin::PROMOTE_K values of k are summed in registers (fp32 outputs).
+template <int BN, bool A_MN, bool B_MN, bool PROMOTE>
 __global__ void __launch_bounds__(lin::THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ LinearArgs a)
@@ -284,28 +352,15 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     LinPipe<BN, A_MN, B_MN> p;
     p.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~static_cast<uintptr_t>(1023));
-    constexpr int STAGES = lin::stages(BN);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + STAGES * lin::stage_bytes(BN));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + lin::stages(BN) * lin::stage_bytes(BN));
     p.bar0 = smem_u32(bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    lin_launch_dependents();
     if (threadIdx.x == 0) {
-        if (a.clear_status && blockIdx.x == 0) { // no wait can have run out yet
-            a.status[0] = DEV_OK;
-            a.status[1] = 0;
-        }
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(p.full(i), 1);
-            mbar_init(p.empty(i), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(p.tfull(i), 1);
-            mbar_init(p.tempty(i), 8);
-        }
-        mbar_init(p.done(), 1);
+        p.init_bars(true);
         *abort_flag = 0;
-        fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
     }
@@ -318,6 +373,12 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int total = a.m_tiles * a.n_tiles;
+    const int run = PROMOTE ? lin::PROMOTE_K / lin::bk(BN) : a.k_blocks;
+    lin_dependency_wait();
+    if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
+        a.status[0] = DEV_OK;
+        a.status[1] = 0;
+    }
 
     if (warp == 0) {
         uint32_t armed = 0;
@@ -329,14 +390,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         p.drain(armed, a.timeout_ns);
     } else if (warp == 1) {
         int it = 0;
-        for (int w = blockIdx.x; w < total; w += gridDim.x, ++it) {
-            const int acc = it & 1;
-            if (!lin_wait(p.tempty(acc), ((it >> 1) & 1) ^ 1, abort_flag, a.timeout_ns, a.status, 520)) break;
-            tc_fence_after();
-            if (!p.multiply(a, tmem + acc * BN, 0, a.k_blocks, abort_flag)) break;
-            if (lin_elect()) umma_commit(p.tfull(acc));
-            __syncwarp();
-        }
+        for (int w = blockIdx.x; w < total; w += gridDim.x)
+            if (!p.multiply_runs(a, tmem, 0, a.k_blocks, run, it, abort_flag)) break;
         if (lin_elect()) umma_commit(p.done()); // every product is finished before TMEM is released
         __syncwarp();
         volatile int never = 0;
@@ -346,39 +401,90 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         const bool gated = a.act == 0;
         const int tc = gated ? BN / 2 : BN;
         const int chunks = tc / 32;
-        const int c0 = half * ((chunks + 1) / 2), c1 = half ? chunks : (chunks + 1) / 2;
+        const int c0 = half * (chunks / 2), c1 = c0 + chunks / 2;
         int it = 0;
-        for (int w = blockIdx.x; w < total; w += gridDim.x, ++it) {
+        bool ok = true;
+        for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
             int mt, nt;
             lin_tile(w, a, mt, nt);
-            const int acc = it & 1;
-            const bool ok = mbar_wait_bounded(p.tfull(acc), (it >> 1) & 1, abort_flag, a.timeout_ns,
-                                              a.status, 540);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
             const int row = mt * lin::BM + q * 32 + lane;
-#pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
-                if (nt * tc + c * 32 >= a.N) break;
-                uint32_t r[32], u[32];
-                tmem_ld_32x32b_x32(t_row + c * 32, r);
-                if (gated) tmem_ld_32x32b_x32(t_row + BN / 2 + c * 32, u);
-                tmem_ld_wait();
+            // the first columns' residual is on its way while the products run
+            uint4 res[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) res[i] = lin_res8(a, row, nt * tc + c0 * 32 + i * 8);
+            auto finish = [&](int c, const float *v32, const float *u32) {
+                uint4 now[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float v[8], x[8];
+                    now[i] = res[i];
+                    if (c + 1 < c1) res[i] = lin_res8(a, row, nt * tc + (c + 1) * 32 + i * 8);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v[8], u[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        v[j] = __uint_as_float(r[i * 8 + j]);
-                        x[j] = gated ? __uint_as_float(u[i * 8 + j]) : 0.0f;
+                        v[j] = v32[i * 8 + j];
+                        u[j] = u32[i * 8 + j];
                     }
-                    lin_finish8(a, row, nt * tc + c * 32 + i * 8, v, x);
+                    lin_finish8(a, row, nt * tc + c * 32 + i * 8, v, u, now[i]);
                 }
+            };
+            if constexpr (PROMOTE) {
+                // this warp's half of the accumulator's columns (SwiGLU: half of the gate's, of the up's)
+                float sum[BN / 2];
+#pragma unroll
+                for (int i = 0; i < BN / 2; ++i) sum[i] = 0.0f;
+                for (int kb = 0; kb < a.k_blocks; kb += run, ++it) {
+                    const int acc = it & 1;
+                    ok = lin_wait(p.tfull(acc), (it >> 1) & 1, abort_flag, a.timeout_ns, a.status, 540);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) {
+                        const int col = gated ? (c < BN / 128 ? c0 + c : BN / 64 + c0 + c - BN / 128) : c0 + c;
+                        lin_add32(t_row, col, sum + c * 32);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p.tempty(acc));
+                }
+                if (!ok) break;
+                if (gated) {
+#pragma unroll
+                    for (int c = 0; c < BN / 128; ++c)
+                        finish(c0 + c, sum + c * 32, sum + (BN / 128 + c) * 32);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) finish(c0 + c, sum + c * 32, sum + c * 32);
+                }
+            } else {
+                const int acc = it & 1;
+                ok = lin_wait(p.tfull(acc), (it >> 1) & 1, abort_flag, a.timeout_ns, a.status, 540);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+#pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
+                    if (nt * tc + c * 32 >= a.N) break;
+                    uint32_t r[32], u[32];
+                    tmem_ld_32x32b_x32(t_row + c * 32, r);
+                    if (gated) tmem_ld_32x32b_x32(t_row + BN / 2 + c * 32, u);
+                    tmem_ld_wait();
+                    float v32[32], u32[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        v32[i] = __uint_as_float(r[i]);
+                        u32[i] = gated ? __uint_as_float(u[i]) : 0.0f;
+                    }
+                    finish(c, v32, u32);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p.tempty(acc));
+                ++it;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p.tempty(acc));
         }
     }
     __syncwarp();
@@ -401,7 +507,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 }
 
 // One tile per cluster of a.splits blocks (launched with that cluster width).
-template <int BN, bool A_MN, bool B_MN>
+template <int BN, bool A_MN, bool B_MN, bool PROMOTE>
 __global__ void __launch_bounds__(lin::THREADS, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ LinearArgs a)
@@ -410,33 +516,25 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     LinPipe<BN, A_MN, B_MN> p;
     p.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~static_cast<uintptr_t>(1023));
-    constexpr int STAGES = lin::stages(BN);
     constexpr int LD = BN + 4; // fp32 row of the parked accumulators: 16-byte writes of 8 rows meet no bank twice
-    static_assert(lin::BM * LD * 4 <= STAGES * lin::stage_bytes(BN), "the parked tile fits the stages");
-    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + STAGES * lin::stage_bytes(BN));
+    constexpr int TMEM_COLS = PROMOTE ? 2 * BN : BN;
+    static_assert(lin::BM * LD * 4 <= lin::stages(BN) * lin::stage_bytes(BN), "the parked tile fits the stages");
+    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + lin::stages(BN) * lin::stage_bytes(BN));
     p.bar0 = smem_u32(bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.splits;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    lin_launch_dependents();
     if (threadIdx.x == 0) {
-        if (a.clear_status && blockIdx.x == 0) {
-            a.status[0] = DEV_OK;
-            a.status[1] = 0;
-        }
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(p.full(i), 1);
-            mbar_init(p.empty(i), 1);
-        }
-        mbar_init(p.tfull(0), 1);
+        p.init_bars(true);
         *abort_flag = 0;
-        fence_mbar_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), BN);
+        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -446,37 +544,76 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     int mt, nt;
     lin_tile(blockIdx.x / S, a, mt, nt);
     const int kb0 = (int)((int64_t)rank * a.k_blocks / S), kb1 = (int)((int64_t)(rank + 1) * a.k_blocks / S);
+    const int run = PROMOTE ? lin::PROMOTE_K / lin::bk(BN) : kb1 - kb0;
     const bool gated = a.act == 0;
     const int tc = gated ? BN / 2 : BN;
     const int rows = min(lin::BM, a.M - mt * lin::BM);
     float *park = reinterpret_cast<float *>(p.smem);
+    lin_dependency_wait();
+    if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
+        a.status[0] = DEV_OK;
+        a.status[1] = 0;
+    }
 
     if (warp == 0) {
         uint32_t armed = 0;
         p.produce(tmA, tmB, a, mt, nt, kb0, kb1, abort_flag, armed);
         p.drain(armed, a.timeout_ns);
     } else if (warp == 1) {
-        p.multiply(a, tmem, kb0, kb1, abort_flag);
-        if (lin_elect()) umma_commit(p.tfull(0)); // every product issued is finished
+        int it = 0;
+        p.multiply_runs(a, tmem, kb0, kb1, run, it, abort_flag);
+        if (lin_elect()) umma_commit(p.done()); // every product issued is finished
         __syncwarp();
     } else {
         const int q = warp & 3, half = warp >= 6 ? 1 : 0;
-        // the products issued finish on their own: this wait ends with them, or runs out
-        volatile int never = 0;
-        const bool ok = mbar_wait_bounded(p.tfull(0), 0, &never, 2 * a.timeout_ns, a.status, 540);
-        if (__all_sync(0xffffffffu, ok) && q * 32 < rows) {
-            tc_fence_after();
-            const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
-            float *dst = park + (q * 32 + lane) * LD;
-#pragma unroll 1
-            for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(t_row + c * 32, r);
-                tmem_ld_wait();
+        bool ok = true;
+        const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16);
+        if constexpr (PROMOTE) {
+            float sum[BN / 2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4 *>(dst + c * 32 + i * 4) =
-                        make_uint4(r[i * 4], r[i * 4 + 1], r[i * 4 + 2], r[i * 4 + 3]);
+            for (int i = 0; i < BN / 2; ++i) sum[i] = 0.0f;
+            int it = 0;
+            for (int kb = kb0; ok && kb < kb1; kb += run, ++it) {
+                const int acc = it & 1;
+                ok = lin_wait(p.tfull(acc), (it >> 1) & 1, abort_flag, a.timeout_ns, a.status, 540);
+                if (!ok) break;
+                if (q * 32 < rows) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c)
+                        lin_add32(t_row + (uint32_t)(acc * BN), half * (BN / 64) + c, sum + c * 32);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p.tempty(acc));
+            }
+            // the stages are free once every product has read them (an abort: once those issued have)
+            volatile int never = 0;
+            ok = lin_wait(p.done(), 0, &never, 2 * a.timeout_ns, a.status, 545);
+            if (ok && q * 32 < rows) {
+                float *dst = park + (q * 32 + lane) * LD + half * (BN / 2);
+#pragma unroll
+                for (int i = 0; i < BN / 8; ++i)
+                    *reinterpret_cast<float4 *>(dst + i * 4) =
+                        make_float4(sum[i * 4], sum[i * 4 + 1], sum[i * 4 + 2], sum[i * 4 + 3]);
+            }
+        } else {
+            // the products issued finish on their own: this wait ends with them, or runs out
+            volatile int never = 0;
+            ok = lin_wait(p.done(), 0, &never, 2 * a.timeout_ns, a.status, 540);
+            if (ok && q * 32 < rows) {
+                tc_fence_after();
+                float *dst = park + (q * 32 + lane) * LD;
+#pragma unroll 1
+                for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t_row + c * 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + c * 32 + i * 4) =
+                            make_uint4(r[i * 4], r[i * 4 + 1], r[i * 4 + 2], r[i * 4 + 3]);
+                }
             }
         }
     }
@@ -488,7 +625,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, BN);
+        tmem_dealloc(tmem, TMEM_COLS);
     }
     if (warp >= 2) {
         // this block's 1/S of the tile's columns, eight at a time
@@ -501,6 +638,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         for (int i = threadIdx.x - 64; i < rows * nv; i += lin::EPI_THREADS) {
             const int row = i / nv, c = (v0 + i - row * nv) * 8;
             if (nt * tc + c >= a.N) continue;
+            const uint4 res = lin_res8(a, mt * lin::BM + row, nt * tc + c);
             const uint32_t off = (uint32_t)(row * LD + c) * 4u;
             float v[8], u[8];
 #pragma unroll
@@ -519,7 +657,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     }
                 }
             }
-            lin_finish8(a, mt * lin::BM + row, nt * tc + c, v, u);
+            lin_finish8(a, mt * lin::BM + row, nt * tc + c, v, u, res);
         }
     }
     if (S > 1) {

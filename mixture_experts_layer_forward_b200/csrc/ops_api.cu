@@ -153,88 +153,95 @@ struct LinearPlan {
     int splits; // 0: the persistent kernel; else blocks per cluster
 };
 
-// Tile width and k split by an estimate of the time of one launch, in SM cycles: a k-block of a
-// 128 x BN tile takes BN cycles of the tensor core, or what its operands take to arrive; a
-// persistent block pays the epilogue once, a split one pays start, reduction and epilogue per
-// tile.
-LinearPlan plan_linear(int64_t M, int64_t n_out, bool gated, int kb, int sms)
+// Tile width and k split by an estimate of the time of one launch, in SM cycles: a 64-value block of
+// k of a 128 x BN tile takes `step` cycles (measured); a persistent block pays start and last
+// epilogue once, a split one pays start, reduction and epilogue per tile. `wide`: 256-column tiles
+// are possible (not for fp32 outputs, whose sums are kept in registers).
+LinearPlan plan_linear(int64_t M, int64_t n_out, bool gated, int64_t K, bool wide, int sms)
 {
     const int ft = g_linear_tile.load(), fs = g_linear_split.load();
-    LinearPlan best{256, 0};
+    LinearPlan best{wide ? 256 : 128, 0};
     double tbest = 1e300;
     const int64_t mt = (M + lin::BM - 1) / lin::BM;
     auto consider = [&](int bn, int s) {
         if (ft != 0 && (bn != ft || s != fs)) return;
         const int tc = gated ? bn / 2 : bn;
         const int64_t tiles = mt * ((n_out + tc - 1) / tc);
-        const double step = bn == 256 ? 290.0 : bn == 128 ? 210.0 : 170.0;
+        const int64_t kb = (K + lin::bk(bn) - 1) / lin::bk(bn);
+        if (s > kb) return;
+        const double step = bn == 256 ? 530.0 : 2.0 * (bn == 128 ? 300.0 : 260.0);
         double t;
         if (s == 0) {
             const int64_t waves = (tiles + sms - 1) / sms;
-            t = 2000.0 + waves * kb * step + 6.0 * bn;
+            t = 4000.0 + waves * kb * step + 8.0 * bn;
         } else {
             const int64_t waves = (tiles * s + sms - 1) / sms;
-            t = waves * (2500.0 + ((kb + s - 1) / s) * step + 6.0 * bn + (s > 1 ? 800.0 + 100.0 * s : 0.0));
+            t = waves * (4500.0 + ((kb + s - 1) / s) * step + 8.0 * bn + (s > 1 ? 800.0 + 100.0 * s : 0.0));
         }
         if (t < tbest) {
             tbest = t;
             best = LinearPlan{bn, s};
         }
     };
-    consider(256, 0);
+    if (wide) consider(256, 0);
     consider(128, 0);
-    for (int s = 1; s <= 8 && s <= kb; s *= 2) {
+    for (int s = 1; s <= 8; s *= 2) {
         consider(128, s);
         if (!gated) consider(64, s);
     }
     return best;
 }
 
-template <int BN, bool A_MN, bool B_MN, bool SPLIT> struct LinearKernel {
-    static cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const LinearArgs &a, int sms,
-                              cudaStream_t st)
-    {
-        constexpr int smem = lin::smem_bytes(BN);
-        if constexpr (!SPLIT) {
-            auto kern = linear_kernel<BN, A_MN, B_MN>;
-            static std::atomic<uint64_t> done{0};
-            const cudaError_t e = prepare((const void *)kern, done);
-            if (e != cudaSuccess) return e;
-            const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
-            kern<<<(unsigned)std::min<int64_t>(tiles, sms), lin::THREADS, smem, st>>>(ta, tb, a);
-            return cudaGetLastError();
-        } else {
-            auto kern = linear_split_kernel<BN, A_MN, B_MN>;
-            static std::atomic<uint64_t> done{0};
-            const cudaError_t e = prepare((const void *)kern, done);
-            if (e != cudaSuccess) return e;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(a.m_tiles * a.n_tiles * a.splits));
-            cfg.blockDim = dim3(lin::THREADS);
-            cfg.dynamicSmemBytes = smem;
-            cfg.stream = st;
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = (unsigned)a.splits;
-            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            return cudaLaunchKernelEx(&cfg, kern, ta, tb, a);
-        }
-    }
+template <int BN, bool A_MN, bool B_MN, bool PROMOTE, bool SPLIT>
+cudaError_t launch_linear_kernel(const CUtensorMap &ta, const CUtensorMap &tb, const LinearArgs &a, int sms,
+                                 cudaStream_t st)
+{
+    void (*kern)(CUtensorMap, CUtensorMap, LinearArgs);
+    if constexpr (SPLIT)
+        kern = linear_split_kernel<BN, A_MN, B_MN, PROMOTE>;
+    else
+        kern = linear_kernel<BN, A_MN, B_MN, PROMOTE>;
     // dynamic shared memory, allowed once per device
-    static cudaError_t prepare(const void *kern, std::atomic<uint64_t> &done)
-    {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 lin::smem_bytes(BN));
         if (e != cudaSuccess) return e;
-        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::smem_bytes(BN));
-        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-        return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-};
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * a.splits : std::min<int64_t>(tiles, sms)));
+    cfg.blockDim = dim3(lin::THREADS);
+    cfg.dynamicSmemBytes = lin::smem_bytes(BN);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    // the next call's blocks are set up while this one's run (they wait for its end before they read)
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)a.splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = SPLIT ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, a);
+}
+
+template <bool A_MN, bool B_MN, bool PROMOTE>
+cudaError_t launch_linear_plan(const LinearPlan &p, const CUtensorMap &ta, const CUtensorMap &tb,
+                               const LinearArgs &a, int sms, cudaStream_t st)
+{
+    if (p.splits != 0)
+        return p.bn == 128 ? launch_linear_kernel<128, A_MN, B_MN, PROMOTE, true>(ta, tb, a, sms, st)
+                           : launch_linear_kernel<64, A_MN, B_MN, PROMOTE, true>(ta, tb, a, sms, st);
+    if constexpr (!PROMOTE)
+        if (p.bn == 256) return launch_linear_kernel<256, A_MN, B_MN, false, false>(ta, tb, a, sms, st);
+    return launch_linear_kernel<128, A_MN, B_MN, PROMOTE, false>(ta, tb, a, sms, st);
+}
 
 // One product of the tile loop. A is [M, K] (K-major) or [K, M] (MN-major), B [N, K] or [K, N];
 // `a` carries M, N, act, epilogue operands and the status word.
@@ -244,9 +251,10 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
 {
     const int sms = sm_count() > 0 ? sm_count() : 148;
     const bool gated = a.act == 0;
-    a.k_blocks = (int)((K + lin::BK - 1) / lin::BK);
-    const LinearPlan p = plan_linear(a.M, a.N, gated, a.k_blocks, sms);
+    const bool promote = a.y_f32 && K > lin::PROMOTE_K;
+    const LinearPlan p = plan_linear(a.M, a.N, gated, K, !promote, sms);
     const int tc = gated ? p.bn / 2 : p.bn;
+    a.k_blocks = (int)((K + lin::bk(p.bn) - 1) / lin::bk(p.bn));
     a.m_tiles = (a.M + lin::BM - 1) / lin::BM;
     a.n_tiles = (a.N + tc - 1) / tc;
     a.group_m = 16;
@@ -254,16 +262,14 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     a.a_rows = std::min(lin::BM, (a.M + 7) / 8 * 8);
     a.timeout_ns = g_timeout_ns.load();
     CUtensorMap ta, tb;
-    const bool ok = (A_MN ? make_map(&ta, A, (uint64_t)K, (uint64_t)a.M, (uint64_t)lda, lin::BK)
+    const bool ok = (A_MN ? make_map(&ta, A, (uint64_t)K, (uint64_t)a.M, (uint64_t)lda, 64)
                           : make_map(&ta, A, (uint64_t)a.M, (uint64_t)K, (uint64_t)lda, (uint32_t)a.a_rows)) &&
-                    (B_MN ? make_map(&tb, B, (uint64_t)K, (uint64_t)b_cols, (uint64_t)ldb, lin::BK)
+                    (B_MN ? make_map(&tb, B, (uint64_t)K, (uint64_t)b_cols, (uint64_t)ldb, 64)
                           : make_map(&tb, B, (uint64_t)b_cols, (uint64_t)K, (uint64_t)ldb, (uint32_t)tc));
     if (!ok) return cudaErrorInvalidValue;
-    if (p.splits == 0)
-        return p.bn == 256 ? LinearKernel<256, A_MN, B_MN, false>::launch(ta, tb, a, sms, st)
-                           : LinearKernel<128, A_MN, B_MN, false>::launch(ta, tb, a, sms, st);
-    return p.bn == 128 ? LinearKernel<128, A_MN, B_MN, true>::launch(ta, tb, a, sms, st)
-                       : LinearKernel<64, A_MN, B_MN, true>::launch(ta, tb, a, sms, st);
+    if constexpr (!A_MN) // gradients of W are bf16
+        if (promote) return launch_linear_plan<A_MN, B_MN, true>(p, ta, tb, a, sms, st);
+    return launch_linear_plan<A_MN, B_MN, false>(p, ta, tb, a, sms, st);
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
