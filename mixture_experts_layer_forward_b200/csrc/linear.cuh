@@ -506,6 +506,31 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
     return v;
 }
 
+// The parked accumulators of linear_split_kernel, for reading by the block that finishes a slice of
+// the columns: slices of BN / S columns one after the other (SwiGLU: a slice's gate half, then its up
+// half), each a dense [128][columns] fp32 block, so that a peer's warp reads 1 KB of consecutive
+// bytes (16-byte reads of scattered rows came to 7 bytes a cycle: 2.3 us for 64 rows at S = 4). The
+// 16-byte units of a row are exchanged by the row's low bits against bank conflicts of the
+// writers, whose lanes hold one row each.
+struct LinPark {
+    int wsh;    // log2 of the columns of a block of the layout
+    int half;   // BN / 2 for SwiGLU, else BN
+    bool gated;
+    __device__ LinPark(int bn, int splits, bool gated_) : gated(gated_)
+    {
+        half = gated ? bn / 2 : bn;
+        wsh = 31 - __clz(half / splits);
+    }
+    // float offset of the 16-byte unit that holds accumulator columns col .. col + 3 of a row
+    __device__ int unit(int row, int col) const
+    {
+        const int up = col >= half ? 1 : 0, c = col - up * half;
+        const int blk = gated ? (c >> wsh) * 2 + up : c >> wsh;
+        const int u = (c & ((1 << wsh) - 1)) >> 2;
+        return (((blk * lin::BM + row) << wsh)) + ((u ^ (row & ((1 << (wsh - 2)) - 1))) << 2);
+    }
+};
+
 // One tile per cluster of a.splits blocks (launched with that cluster width).
 template <int BN, bool A_MN, bool B_MN, bool PROMOTE>
 __global__ void __launch_bounds__(lin::THREADS, 1)
@@ -516,9 +541,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     LinPipe<BN, A_MN, B_MN> p;
     p.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~static_cast<uintptr_t>(1023));
-    constexpr int LD = BN + 4; // fp32 row of the parked accumulators: 16-byte writes of 8 rows meet no bank twice
     constexpr int TMEM_COLS = PROMOTE ? 2 * BN : BN;
-    static_assert(lin::BM * LD * 4 <= lin::stages(BN) * lin::stage_bytes(BN), "the parked tile fits the stages");
+    static_assert(lin::BM * BN * 4 <= lin::stages(BN) * lin::stage_bytes(BN), "the parked tile fits the stages");
     uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + lin::stages(BN) * lin::stage_bytes(BN));
     p.bar0 = smem_u32(bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
@@ -549,6 +573,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int tc = gated ? BN / 2 : BN;
     const int rows = min(lin::BM, a.M - mt * lin::BM);
     float *park = reinterpret_cast<float *>(p.smem);
+    const LinPark lay(BN, S, gated);
     lin_dependency_wait();
     if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
         a.status[0] = DEV_OK;
@@ -591,10 +616,10 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
             volatile int never = 0;
             ok = lin_wait(p.done(), 0, &never, 2 * a.timeout_ns, a.status, 545);
             if (ok && q * 32 < rows) {
-                float *dst = park + (q * 32 + lane) * LD + half * (BN / 2);
+                const int row = q * 32 + lane;
 #pragma unroll
                 for (int i = 0; i < BN / 8; ++i)
-                    *reinterpret_cast<float4 *>(dst + i * 4) =
+                    *reinterpret_cast<float4 *>(park + lay.unit(row, half * (BN / 2) + i * 4)) =
                         make_float4(sum[i * 4], sum[i * 4 + 1], sum[i * 4 + 2], sum[i * 4 + 3]);
             }
         } else {
@@ -603,7 +628,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
             ok = lin_wait(p.done(), 0, &never, 2 * a.timeout_ns, a.status, 540);
             if (ok && q * 32 < rows) {
                 tc_fence_after();
-                float *dst = park + (q * 32 + lane) * LD;
+                const int row = q * 32 + lane;
 #pragma unroll 1
                 for (int c = half * (BN / 64); c < (half + 1) * (BN / 64); ++c) {
                     uint32_t r[32];
@@ -611,7 +636,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(dst + c * 32 + i * 4) =
+                        *reinterpret_cast<uint4 *>(park + lay.unit(row, c * 32 + i * 4)) =
                             make_uint4(r[i * 4], r[i * 4 + 1], r[i * 4 + 2], r[i * 4 + 3]);
                 }
             }
@@ -629,31 +654,48 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     }
     if (warp >= 2) {
         // this block's 1/S of the tile's columns, eight at a time
-        const int vec = tc / 8;
-        const int v0 = rank * vec / S, nv = (rank + 1) * vec / S - v0;
+        const int vsh = lay.wsh - 3; // log2 of the 8-column pieces of a row
         const uint32_t base = smem_u32(park);
         uint32_t peer[8];
 #pragma unroll
         for (int s = 0; s < 8; ++s) peer[s] = (S > 1 && s < S) ? mapa_shared(base, (uint32_t)s) : base;
-        for (int i = threadIdx.x - 64; i < rows * nv; i += lin::EPI_THREADS) {
-            const int row = i / nv, c = (v0 + i - row * nv) * 8;
+        const int block0 = rank * (gated ? 2 : 1); // this slice's (gate) block of the layout
+        for (int i = threadIdx.x - 64; i < (rows << vsh); i += lin::EPI_THREADS) {
+            // 32 consecutive bytes of the layout: row, and the piece it holds there (its two 16-byte
+            // units swapped in odd rows)
+            const int row = i >> vsh, at = i & ((1 << vsh) - 1);
+            const int piece = at ^ ((row >> 1) & ((1 << vsh) - 1));
+            const int c = (rank << lay.wsh) + piece * 8;
             if (nt * tc + c >= a.N) continue;
             const uint4 res = lin_res8(a, mt * lin::BM + row, nt * tc + c);
-            const uint32_t off = (uint32_t)(row * LD + c) * 4u;
+            const uint32_t off = (uint32_t)(((block0 * lin::BM + row) << lay.wsh) + at * 8) * 4u;
+            const uint32_t lo = off + ((row & 1) << 4), hi = off + (((row & 1) ^ 1) << 4);
+            const uint32_t up = (uint32_t)(lin::BM << lay.wsh) * 4u;
             float v[8], u[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.0f;
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                if (s < S) {
-                    const float4 x0 = ld_cluster_f4(peer[s] + off), x1 = ld_cluster_f4(peer[s] + off + 16);
-                    v[0] += x0.x; v[1] += x0.y; v[2] += x0.z; v[3] += x0.w;
-                    v[4] += x1.x; v[5] += x1.y; v[6] += x1.z; v[7] += x1.w;
+            for (int s0 = 0; s0 < 8; s0 += 4) { // four peers' parts in flight, added in rank order
+                if (s0 >= S) break;
+                float4 x[4][4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (s0 + s >= S) break;
+                    x[s][0] = ld_cluster_f4(peer[s0 + s] + lo);
+                    x[s][1] = ld_cluster_f4(peer[s0 + s] + hi);
                     if (gated) {
-                        const float4 y0 = ld_cluster_f4(peer[s] + off + BN * 2);
-                        const float4 y1 = ld_cluster_f4(peer[s] + off + BN * 2 + 16);
-                        u[0] += y0.x; u[1] += y0.y; u[2] += y0.z; u[3] += y0.w;
-                        u[4] += y1.x; u[5] += y1.y; u[6] += y1.z; u[7] += y1.w;
+                        x[s][2] = ld_cluster_f4(peer[s0 + s] + lo + up);
+                        x[s][3] = ld_cluster_f4(peer[s0 + s] + hi + up);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (s0 + s >= S) break;
+                    v[0] += x[s][0].x; v[1] += x[s][0].y; v[2] += x[s][0].z; v[3] += x[s][0].w;
+                    v[4] += x[s][1].x; v[5] += x[s][1].y; v[6] += x[s][1].z; v[7] += x[s][1].w;
+                    if (gated) {
+                        u[0] += x[s][2].x; u[1] += x[s][2].y; u[2] += x[s][2].z; u[3] += x[s][2].w;
+                        u[4] += x[s][3].x; u[5] += x[s][3].y; u[6] += x[s][3].z; u[7] += x[s][3].w;
                     }
                 }
             }
