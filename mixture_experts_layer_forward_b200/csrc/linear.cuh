@@ -44,7 +44,11 @@ __host__ __device__ constexpr int bk(int bn) { return 64 * sub(bn); }
 __host__ __device__ constexpr int stage_bytes(int bn) { return sub(bn) * (A_BOX + bn * 128); }
 __host__ __device__ constexpr int stages(int bn) { return 196608 / stage_bytes(bn); } // 4, 3, 4 for BN = 256, 128, 64
 __host__ __device__ constexpr int num_bars(int bn) { return 2 * stages(bn) + 5; }
-__host__ __device__ constexpr int smem_bytes(int bn) { return 1024 + stages(bn) * stage_bytes(bn) + num_bars(bn) * 8 + 16; }
+constexpr int TURN = 32 * 32 * 4; // one warp's 32 x 32 fp32 values on their way from rows per lane to rows in memory
+__host__ __device__ constexpr int smem_bytes(int bn, bool split)
+{
+    return 1024 + stages(bn) * stage_bytes(bn) + (split ? 0 : 8 * TURN) + num_bars(bn) * 8 + 16;
+}
 // fp32 outputs: k values summed in one accumulator before its values are added up in registers (the
 // tensor core adds to an accumulator by truncation, about 2^-26 of it a step of 16: 3.8e-6 over
 // K = 7168, 5e-7 over 512)
@@ -67,6 +71,9 @@ struct LinearArgs {
     __nv_bfloat16 *z;     // pre-activation [M, N or 2N], row stride ldz, or nullptr
     int64_t ldz;
     int splits;           // linear_split_kernel: blocks per cluster
+    int ahead;            // the blocks bring both operands into L2 as the launch starts
+    const void *a_ptr, *b_ptr;   // the operands, for that: rows, bytes of a row, bytes from row to row
+    int64_t a_num, a_row, a_ld, b_num, b_row, b_ld;
     int *status;
     int clear_status;     // block 0 clears the status word (the call's first launch with waits)
     int64_t timeout_ns;
@@ -331,15 +338,47 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
     }
 };
 
-// One warp's part of a finished run: 32 rows (TMEM lanes q * 32 ..), columns [c * 32, c * 32 + 32) of the
-// accumulator, added to sum.
-__device__ __forceinline__ void lin_add32(uint32_t t_row, int c, float *sum)
+// Part `part` of `parts` of a matrix into L2, a 128-byte line per thread and turn. Where several
+// blocks read each operand tile at the same time and few tiles run, the copies' depth does not
+// cover the memory's latency (a k-block of 88 tiles took 0.62 us instead of 0.28).
+__device__ __forceinline__ void lin_ahead(const void *base, int64_t num, int64_t row, int64_t ld, int part,
+                                          int parts, int tid, int threads)
 {
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(t_row + c * 32, r);
+    const int64_t lines = (row + 127) / 128 + 1; // rows start anywhere in a line
+    const int64_t total = num * lines, lo = total * part / parts, hi = total * (part + 1) / parts;
+    for (int64_t i = lo + tid; i < hi; i += threads) {
+        const int64_t r = i / lines, at = (i - r * lines) * 128;
+        const char *p = static_cast<const char *>(base) + r * ld + (at < row ? at : row - 1);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    }
+}
+
+// 16 consecutive accumulator columns of this warp's 32 rows (one row per lane), to be waited for
+// before they are used.
+__device__ __forceinline__ void lin_ld16(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// A finished run's columns added to sum.
+__device__ __forceinline__ void lin_add16(uint32_t taddr, float *sum)
+{
+    uint32_t r[16];
+    lin_ld16(taddr, r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void lin_add32(uint32_t t_row, int c, float *sum)
+{
+    lin_add16(t_row + c * 32, sum);
+    lin_add16(t_row + c * 32 + 16, sum + 16);
 }
 
 // PROMOTE: runs of lin::PROMOTE_K values of k are summed in registers (fp32 outputs).
@@ -352,12 +391,17 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     LinPipe<BN, A_MN, B_MN> p;
     p.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(p.smem + lin::stages(BN) * lin::stage_bytes(BN));
+    float *turns = reinterpret_cast<float *>(p.smem + lin::stages(BN) * lin::stage_bytes(BN));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(turns + 8 * lin::TURN / 4);
     p.bar0 = smem_u32(bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     lin_launch_dependents();
+    if (warp >= 2 && a.ahead) {
+        lin_ahead(a.a_ptr, a.a_num, a.a_row, a.a_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
+        lin_ahead(a.b_ptr, a.b_num, a.b_row, a.b_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
+    }
     if (threadIdx.x == 0) {
         p.init_bars(true);
         *abort_flag = 0;
@@ -400,34 +444,48 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         const int q = warp & 3, half = warp >= 6 ? 1 : 0;
         const bool gated = a.act == 0;
         const int tc = gated ? BN / 2 : BN;
-        const int chunks = tc / 32;
-        const int c0 = half * (chunks / 2), c1 = c0 + chunks / 2;
         int it = 0;
         bool ok = true;
         for (int w = blockIdx.x; ok && w < total; w += gridDim.x) {
             int mt, nt;
             lin_tile(w, a, mt, nt);
-            const int row = mt * lin::BM + q * 32 + lane;
-            // the first columns' residual is on its way while the products run
-            uint4 res[4];
+            // A lane's accumulators are one row of 32 values (SwiGLU: 16 gate and 16 up columns); in
+            // memory the warp takes whole rows' pieces, eight columns a lane, so that loads and stores
+            // touch whole sectors of few lines (one row per lane: 32 lines an instruction). The values
+            // change hands through shared memory, their 16-byte units exchanged by the row's low bits.
+            // The loop over the rows stays rolled: its code runs a few times a launch, and unrolled
+            // it was fetched more slowly than it ran (4 us a tile instead of 2).
+            float *turn = turns + (warp - 2) * (lin::TURN / 4);
+            const int psh = gated ? 1 : 2;                   // log2 of the lanes (8-column pieces) of a row
+            const int piece = lane & ((1 << psh) - 1), up_unit = 4 + piece * 2;
+            const int cols = 8 << psh;                       // output columns of a turn
+            const int first = nt * tc + half * (tc / 2);     // this warp's first column
+            auto own_row = [&](const uint32_t (&own)[32]) {  // 32 values of row `lane` into the turn
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) res[i] = lin_res8(a, row, nt * tc + c0 * 32 + i * 8);
-            auto finish = [&](int c, const float *v32, const float *u32) {
-                uint4 now[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    now[i] = res[i];
-                    if (c + 1 < c1) res[i] = lin_res8(a, row, nt * tc + (c + 1) * 32 + i * 8);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(turn + lane * 32 + ((i ^ (lane & 7)) << 2)) =
+                        make_uint4(own[i * 4], own[i * 4 + 1], own[i * 4 + 2], own[i * 4 + 3]);
+                __syncwarp();
+            };
+            auto rows_out = [&](int col) {                   // the turn's 32 rows, columns col .. col + cols
+                int r = lane >> psh;
+                const int row0 = mt * lin::BM + q * 32;
+                uint4 res = lin_res8(a, row0 + r, col + piece * 8);
+#pragma unroll 1
+                for (; r < 32; r += 32 >> psh) {
+                    const uint4 now = res;
+                    if (r + (32 >> psh) < 32) res = lin_res8(a, row0 + r + (32 >> psh), col + piece * 8);
                     float v[8], u[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[j] = v32[i * 8 + j];
-                        u[j] = u32[i * 8 + j];
-                    }
-                    lin_finish8(a, row, nt * tc + c * 32 + i * 8, v, u, now[i]);
+                    auto take = [&](int unit, float (&o)[8]) {
+                        const float4 x = *reinterpret_cast<const float4 *>(turn + r * 32 + ((unit ^ (r & 7)) << 2));
+                        const float4 y = *reinterpret_cast<const float4 *>(turn + r * 32 + (((unit + 1) ^ (r & 7)) << 2));
+                        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+                        o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+                    };
+                    take(piece * 2, v);
+                    if (gated) take(up_unit, u);
+                    lin_finish8(a, row0 + r, col + piece * 8, v, u, now);
                 }
             };
             if constexpr (PROMOTE) {
@@ -441,23 +499,29 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+                    if (gated) { // turns of 16 gate and 16 up columns
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) {
-                        const int col = gated ? (c < BN / 128 ? c0 + c : BN / 64 + c0 + c - BN / 128) : c0 + c;
-                        lin_add32(t_row, col, sum + c * 32);
+                        for (int c = 0; c < BN / 64; ++c) {
+                            lin_add16(t_row + half * (BN / 4) + c * 16, sum + c * 32);
+                            lin_add16(t_row + BN / 2 + half * (BN / 4) + c * 16, sum + c * 32 + 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < BN / 64; ++c)
+                            lin_add32(t_row, half * (BN / 64) + c, sum + c * 32);
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p.tempty(acc));
                 }
                 if (!ok) break;
-                if (gated) {
 #pragma unroll
-                    for (int c = 0; c < BN / 128; ++c)
-                        finish(c0 + c, sum + c * 32, sum + (BN / 128 + c) * 32);
-                } else {
+                for (int c = 0; c < BN / 64; ++c) {
+                    uint32_t own[32];
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) finish(c0 + c, sum + c * 32, sum + c * 32);
+                    for (int i = 0; i < 32; ++i) own[i] = __float_as_uint(sum[c * 32 + i]);
+                    own_row(own);
+                    rows_out(first + c * cols);
                 }
             } else {
                 const int acc = it & 1;
@@ -465,20 +529,21 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+                const uint32_t t_col = t_row + half * (tc / 2);
 #pragma unroll 1
-                for (int c = c0; c < c1; ++c) {
-                    if (nt * tc + c * 32 >= a.N) break;
-                    uint32_t r[32], u[32];
-                    tmem_ld_32x32b_x32(t_row + c * 32, r);
-                    if (gated) tmem_ld_32x32b_x32(t_row + BN / 2 + c * 32, u);
-                    tmem_ld_wait();
-                    float v32[32], u32[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        v32[i] = __uint_as_float(r[i]);
-                        u32[i] = gated ? __uint_as_float(u[i]) : 0.0f;
+                for (int c = 0; c < tc / 2; c += cols) {
+                    if (first + c >= a.N) break;
+                    uint32_t own[32];
+                    if (gated) {
+                        lin_ld16(t_col + c, own);
+                        lin_ld16(t_col + BN / 2 + c, own + 16);
+                    } else {
+                        lin_ld16(t_col + c, own);
+                        lin_ld16(t_col + c + 16, own + 16);
                     }
-                    finish(c, v32, u32);
+                    tmem_ld_wait();
+                    own_row(own);
+                    rows_out(first + c);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -551,6 +616,10 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int S = a.splits;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     lin_launch_dependents();
+    if (warp >= 2 && a.ahead) {
+        lin_ahead(a.a_ptr, a.a_num, a.a_row, a.a_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
+        lin_ahead(a.b_ptr, a.b_num, a.b_row, a.b_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
+    }
     if (threadIdx.x == 0) {
         p.init_bars(true);
         *abort_flag = 0;

@@ -209,7 +209,7 @@ cudaError_t launch_linear_kernel(const CUtensorMap &ta, const CUtensorMap &tb, c
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!(allowed.load(std::memory_order_relaxed) & bit)) {
         e = cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 lin::smem_bytes(BN));
+                                 lin::smem_bytes(BN, SPLIT));
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -217,7 +217,7 @@ cudaError_t launch_linear_kernel(const CUtensorMap &ta, const CUtensorMap &tb, c
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * a.splits : std::min<int64_t>(tiles, sms)));
     cfg.blockDim = dim3(lin::THREADS);
-    cfg.dynamicSmemBytes = lin::smem_bytes(BN);
+    cfg.dynamicSmemBytes = lin::smem_bytes(BN, SPLIT);
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     // the next call's blocks are set up while this one's run (they wait for its end before they read)
@@ -261,6 +261,17 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     a.splits = p.splits;
     a.a_rows = std::min(lin::BM, (a.M + 7) / 8 * 8);
     a.timeout_ns = g_timeout_ns.load();
+    a.a_ptr = A;
+    a.a_num = A_MN ? K : a.M;
+    a.a_row = 2 * (A_MN ? (int64_t)a.M : K);
+    a.a_ld = 2 * lda;
+    a.b_ptr = B;
+    a.b_num = B_MN ? K : b_cols;
+    a.b_row = 2 * (B_MN ? b_cols : K);
+    a.b_ld = 2 * ldb;
+    // few tiles that share their operands: latency, not rate, bounds their copies
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    a.ahead = a.m_tiles > 1 && tiles <= 2 * sms && a.a_num * a.a_row + a.b_num * a.b_row <= (32 << 20);
     CUtensorMap ta, tb;
     const bool ok = (A_MN ? make_map(&ta, A, (uint64_t)K, (uint64_t)a.M, (uint64_t)lda, 64)
                           : make_map(&ta, A, (uint64_t)a.M, (uint64_t)K, (uint64_t)lda, (uint32_t)a.a_rows)) &&
