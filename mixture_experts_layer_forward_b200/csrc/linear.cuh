@@ -79,18 +79,23 @@ struct LinearArgs {
     int64_t timeout_ns;
 };
 
-__device__ __forceinline__ void lin_bias8(const float *bias, float (&v)[8])
+__device__ __forceinline__ void lin_load_bias8(const float *bias, float (&b)[8])
 {
-    const float4 a = reinterpret_cast<const float4 *>(bias)[0];
-    const float4 b = reinterpret_cast<const float4 *>(bias)[1];
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    const float4 x = reinterpret_cast<const float4 *>(bias)[0];
+    const float4 y = reinterpret_cast<const float4 *>(bias)[1];
+    b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
+    b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
 }
 
+__device__ __forceinline__ uint32_t lin_pack2(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
 __device__ __forceinline__ uint4 lin_pack8(const float (&v)[8])
 {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
+    return make_uint4(lin_pack2(v[0], v[1]), lin_pack2(v[2], v[3]), lin_pack2(v[4], v[5]),
+                      lin_pack2(v[6], v[7]));
 }
 
 // z * sigmoid(c z') forms with the fast exponential: its error reaches the product scaled by
@@ -109,44 +114,53 @@ __device__ __forceinline__ uint4 lin_res8(const LinearArgs &a, int row, int col)
     return *reinterpret_cast<const uint4 *>(a.res + (size_t)row * a.ldr + col);
 }
 
-// Eight consecutive output columns of one row (col % 8 == 0, N % 8 == 0): v the accumulators
-// (SwiGLU: v the gate's, u the up's), r the residual, loaded ahead.
-__device__ __forceinline__ void lin_finish8(const LinearArgs &a, int row, int col, float (&v)[8],
-                                            float (&u)[8], const uint4 &r)
+// Where eight consecutive output columns of one row go (z of SwiGLU: the up half up_col further).
+struct LinOut {
+    char *y;            // bf16 or fp32
+    __nv_bfloat16 *z;   // nullptr: not wanted
+    __device__ LinOut(const LinearArgs &a, int row, int col)
+    {
+        y = static_cast<char *>(a.y) + ((size_t)row * a.ldy + col) * (a.y_f32 ? 4 : 2);
+        z = a.z != nullptr ? a.z + (size_t)row * a.ldz + col : nullptr;
+    }
+    __device__ void down(const LinearArgs &a, int rows)
+    {
+        y += (size_t)rows * a.ldy * (a.y_f32 ? 4 : 2);
+        if (z != nullptr) z += (size_t)rows * a.ldz;
+    }
+};
+
+// Eight consecutive columns of one row: v the accumulators (SwiGLU: v the gate's, u the up's), bv and
+// bu the bias (zeros: none), r the residual.
+__device__ __forceinline__ void lin_finish8(const LinearArgs &a, float (&v)[8], float (&u)[8],
+                                            const float (&bv)[8], const float (&bu)[8], const uint4 &r,
+                                            const LinOut &out)
 {
-    if (row >= a.M || col >= a.N) return;
-    if (a.bias != nullptr) lin_bias8(a.bias + col, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += bv[i];
+    if (out.z != nullptr) *reinterpret_cast<uint4 *>(out.z) = lin_pack8(v);
     if (a.act == 0) {
-        if (a.bias != nullptr) lin_bias8(a.bias + a.up_col + col, u);
-        if (a.z != nullptr) {
-            __nv_bfloat16 *zr = a.z + (size_t)row * a.ldz + col;
-            *reinterpret_cast<uint4 *>(zr) = lin_pack8(v);
-            *reinterpret_cast<uint4 *>(zr + a.up_col) = lin_pack8(u);
-        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += bu[i];
+        if (out.z != nullptr) *reinterpret_cast<uint4 *>(out.z + a.up_col) = lin_pack8(u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = lin_silu(v[i]) * u[i];
-    } else {
-        if (a.z != nullptr)
-            *reinterpret_cast<uint4 *>(a.z + (size_t)row * a.ldz + col) = lin_pack8(v);
-        if (a.act == 1) {
+    } else if (a.act == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = lin_gelu(v[i]);
-        } else if (a.act == 2) {
+        for (int i = 0; i < 8; ++i) v[i] = lin_gelu(v[i]);
+    } else if (a.act == 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
-        }
+        for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
     }
     if (a.res != nullptr) {
         v[0] += bf16_lo(r.x); v[1] += bf16_hi(r.x); v[2] += bf16_lo(r.y); v[3] += bf16_hi(r.y);
         v[4] += bf16_lo(r.z); v[5] += bf16_hi(r.z); v[6] += bf16_lo(r.w); v[7] += bf16_hi(r.w);
     }
     if (a.y_f32) {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + (size_t)row * a.ldy + col);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+        reinterpret_cast<float4 *>(out.y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(out.y)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.y) + (size_t)row * a.ldy + col) =
-            lin_pack8(v);
+        *reinterpret_cast<uint4 *>(out.y) = lin_pack8(v);
     }
 }
 
@@ -468,14 +482,36 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                         make_uint4(own[i * 4], own[i * 4 + 1], own[i * 4 + 2], own[i * 4 + 3]);
                 __syncwarp();
             };
-            auto rows_out = [&](int col) {                   // the turn's 32 rows, columns col .. col + cols
-                int r = lane >> psh;
-                const int row0 = mt * lin::BM + q * 32;
-                uint4 res = lin_res8(a, row0 + r, col + piece * 8);
+            const int rstep = 32 >> psh, row0 = mt * lin::BM + q * 32 + (lane >> psh);
+            // the residual of this lane's rows of a turn, on its way one turn ahead (the first turn's
+            // while the products run)
+            uint4 res[4] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u),
+                            make_uint4(0u, 0u, 0u, 0u)};
+            auto fetch = [&](int col) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    res[i] = i < (1 << psh) ? lin_res8(a, row0 + i * rstep, col + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
+            };
+            if (a.res != nullptr) fetch(first);
+            auto rows_out = [&](int col, bool more) {        // the turn's 32 rows, columns col .. col + cols
+                uint4 now[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = res[i];
+                if (more && a.res != nullptr) fetch(col + cols);
+                const int mine = col + piece * 8;
+                if (mine >= a.N) return;
+                float bv[8], bu[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bv[i] = bu[i] = 0.0f;
+                if (a.bias != nullptr) {
+                    lin_load_bias8(a.bias + mine, bv);
+                    if (gated) lin_load_bias8(a.bias + a.up_col + mine, bu);
+                }
+                LinOut out(a, row0, mine);
 #pragma unroll 1
-                for (; r < 32; r += 32 >> psh) {
-                    const uint4 now = res;
-                    if (r + (32 >> psh) < 32) res = lin_res8(a, row0 + r + (32 >> psh), col + piece * 8);
+                for (int i = 0; i < (1 << psh); ++i) {
+                    if (row0 + i * rstep >= a.M) break;
+                    const int r = (lane >> psh) + i * rstep;
                     float v[8], u[8];
                     auto take = [&](int unit, float (&o)[8]) {
                         const float4 x = *reinterpret_cast<const float4 *>(turn + r * 32 + ((unit ^ (r & 7)) << 2));
@@ -485,7 +521,11 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     };
                     take(piece * 2, v);
                     if (gated) take(up_unit, u);
-                    lin_finish8(a, row0 + r, col + piece * 8, v, u, now);
+                    lin_finish8(a, v, u, bv, bu, now[0], out);
+                    out.down(a, rstep);
+                    now[0] = now[1];
+                    now[1] = now[2];
+                    now[2] = now[3];
                 }
             };
             if constexpr (PROMOTE) {
@@ -521,7 +561,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) own[i] = __float_as_uint(sum[c * 32 + i]);
                     own_row(own);
-                    rows_out(first + c * cols);
+                    rows_out(first + c * cols, c + 1 < BN / 64);
                 }
             } else {
                 const int acc = it & 1;
@@ -543,7 +583,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     }
                     tmem_ld_wait();
                     own_row(own);
-                    rows_out(first + c);
+                    rows_out(first + c, c + cols < tc / 2);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -768,7 +808,14 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     }
                 }
             }
-            lin_finish8(a, mt * lin::BM + row, nt * tc + c, v, u, res);
+            float bv[8], bu[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bv[j] = bu[j] = 0.0f;
+            if (a.bias != nullptr) {
+                lin_load_bias8(a.bias + nt * tc + c, bv);
+                if (gated) lin_load_bias8(a.bias + a.up_col + nt * tc + c, bu);
+            }
+            lin_finish8(a, v, u, bv, bu, res, LinOut(a, mt * lin::BM + row, nt * tc + c));
         }
     }
     if (S > 1) {
