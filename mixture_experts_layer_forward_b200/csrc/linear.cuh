@@ -71,9 +71,6 @@ struct LinearArgs {
     __nv_bfloat16 *z;     // pre-activation [M, N or 2N], row stride ldz, or nullptr
     int64_t ldz;
     int splits;           // linear_split_kernel: blocks per cluster
-    int ahead;            // the blocks bring both operands into L2 as the launch starts
-    const void *a_ptr, *b_ptr;   // the operands, for that: rows, bytes of a row, bytes from row to row
-    int64_t a_num, a_row, a_ld, b_num, b_row, b_ld;
     int *status;
     int clear_status;     // block 0 clears the status word (the call's first launch with waits)
     int64_t timeout_ns;
@@ -98,13 +95,36 @@ __device__ __forceinline__ uint4 lin_pack8(const float (&v)[8])
                       lin_pack2(v[6], v[7]));
 }
 
-// z * sigmoid(c z') forms with the fast exponential: its error reaches the product scaled by
-// the sigmoid, about 2^-22 of the value
-__device__ __forceinline__ float lin_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-__device__ __forceinline__ float lin_gelu(float z)
+// 2^x and 1 / x of the special function unit (2^-22.5 and 2^-23 relative; denormal results 0)
+__device__ __forceinline__ float lin_ex2(float x)
 {
-    const float c2 = 1.5957691216057308f; // 2 sqrt(2 / pi): (1 + tanh(w)) / 2 = 1 / (1 + exp(-2 w))
-    return __fdividef(z, 1.0f + __expf(-c2 * (z + 0.044715f * z * z * z)));
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lin_rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float LIN_LOG2E = 1.4426950408889634f;
+constexpr float LIN_GC2 = 1.5957691216057308f; // 2 sqrt(2 / pi): (1 + tanh(w)) / 2 = 1 / (1 + exp(-2 w))
+constexpr float LIN_GK = 0.044715f;
+
+__device__ __forceinline__ float lin_sigmoid(float z) { return lin_rcp(1.0f + lin_ex2(-LIN_LOG2E * z)); }
+// the sigmoid of 2 sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float lin_gelu_gate(float z, float z2)
+{
+    return lin_rcp(1.0f + lin_ex2(z * fmaf(-LIN_LOG2E * LIN_GC2 * LIN_GK, z2, -LIN_LOG2E * LIN_GC2)));
+}
+__device__ __forceinline__ float lin_silu(float z) { return z * lin_sigmoid(z); }
+__device__ __forceinline__ float lin_gelu(float z) { return z * lin_gelu_gate(z, z * z); }
+// s + z s (1 - s) w', w' = 2 sqrt(2 / pi) (1 + 3 * 0.044715 z^2)
+__device__ __forceinline__ float lin_gelu_grad(float z)
+{
+    const float z2 = z * z, s = lin_gelu_gate(z, z2);
+    return s * fmaf(z * (1.0f - s), fmaf(3.0f * LIN_GK * LIN_GC2, z2, LIN_GC2), 1.0f);
 }
 
 // The residual of eight columns (zeros outside the output).
@@ -352,21 +372,6 @@ template <int BN, bool A_MN, bool B_MN> struct LinPipe {
     }
 };
 
-// Part `part` of `parts` of a matrix into L2, a 128-byte line per thread and turn. Where several
-// blocks read each operand tile at the same time and few tiles run, the copies' depth does not
-// cover the memory's latency (a k-block of 88 tiles took 0.62 us instead of 0.28).
-__device__ __forceinline__ void lin_ahead(const void *base, int64_t num, int64_t row, int64_t ld, int part,
-                                          int parts, int tid, int threads)
-{
-    const int64_t lines = (row + 127) / 128 + 1; // rows start anywhere in a line
-    const int64_t total = num * lines, lo = total * part / parts, hi = total * (part + 1) / parts;
-    for (int64_t i = lo + tid; i < hi; i += threads) {
-        const int64_t r = i / lines, at = (i - r * lines) * 128;
-        const char *p = static_cast<const char *>(base) + r * ld + (at < row ? at : row - 1);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-    }
-}
-
 // 16 consecutive accumulator columns of this warp's 32 rows (one row per lane), to be waited for
 // before they are used.
 __device__ __forceinline__ void lin_ld16(uint32_t taddr, uint32_t *r)
@@ -412,10 +417,6 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     lin_launch_dependents();
-    if (warp >= 2 && a.ahead) {
-        lin_ahead(a.a_ptr, a.a_num, a.a_row, a.a_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
-        lin_ahead(a.b_ptr, a.b_num, a.b_row, a.b_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
-    }
     if (threadIdx.x == 0) {
         p.init_bars(true);
         *abort_flag = 0;
@@ -656,10 +657,6 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int S = a.splits;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     lin_launch_dependents();
-    if (warp >= 2 && a.ahead) {
-        lin_ahead(a.a_ptr, a.a_num, a.a_row, a.a_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
-        lin_ahead(a.b_ptr, a.b_num, a.b_row, a.b_ld, blockIdx.x, gridDim.x, threadIdx.x - 64, lin::EPI_THREADS);
-    }
     if (threadIdx.x == 0) {
         p.init_bars(true);
         *abort_flag = 0;
@@ -836,84 +833,90 @@ struct LinearDzArgs {
     int64_t ldz;
     __nv_bfloat16 *dz;      // [M, N or 2N] dense, or nullptr (only the column sums are wanted)
     float *part;            // [chunks, N or 2N] column sums of each row chunk, or nullptr
-    int M, N, act;
+    int M, N;
     int rows;               // rows per chunk
 };
 
-__device__ __forceinline__ float lin_gelu_grad(float z)
-{
-    const float c2 = 1.5957691216057308f;
-    const float s = __fdividef(1.0f, 1.0f + __expf(-c2 * (z + 0.044715f * z * z * z)));
-    return s + z * s * (1.0f - s) * c2 * (1.0f + 3.0f * 0.044715f * z * z);
-}
-
 // dz (bf16, the products' operand) and the column sums of the unrounded dz, in one pass over dy
-// and z. A block has 32 x 8 threads: 32 vectors of eight columns, eight rows at a time; the
-// sums over a chunk's rows run in fp32 in a fixed order (rows of one thread, then the eight
-// threads). Bound by the bytes of dy, z and dz.
+// and z. A block has 32 x 8 threads: 32 vectors of eight columns, sixteen rows at a time (two a
+// thread, their loads in flight together); the sums over a chunk's rows run in fp32 in a fixed order
+// (rows of one thread, then the eight threads). Bound by the bytes of dy, z and dz.
+template <int ACT, bool F32>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ LinearDzArgs a)
 {
+    constexpr bool GATED = ACT == 0;
+    constexpr int ND = F32 ? 2 : 1; // 16-byte pieces of eight dy
     __shared__ float red[8][32][17];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int col = (blockIdx.x * 32 + tx) * 8;
-    const bool gated = a.act == 0;
-    const int cols = gated ? 2 * a.N : a.N;
+    const int cols = GATED ? 2 * a.N : a.N;
     const int r1 = min(a.M, ((int)blockIdx.y + 1) * a.rows);
     float sg[8], su[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+    struct Row {
+        uint4 d[ND], g, u;
+    };
+    auto load = [&](int row, Row &x) {
+        const char *p = static_cast<const char *>(a.dy) + ((size_t)row * a.ldy + col) * (F32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < ND; ++i) x.d[i] = reinterpret_cast<const uint4 *>(p)[i];
+        if (ACT != 3) {
+            const __nv_bfloat16 *zr = a.z + (size_t)row * a.ldz + col;
+            x.g = *reinterpret_cast<const uint4 *>(zr);
+            if (GATED) x.u = *reinterpret_cast<const uint4 *>(zr + a.N);
+        }
+    };
+    auto unpack = [](const uint4 &x, float (&v)[8]) {
+        v[0] = bf16_lo(x.x); v[1] = bf16_hi(x.x); v[2] = bf16_lo(x.y); v[3] = bf16_hi(x.y);
+        v[4] = bf16_lo(x.z); v[5] = bf16_hi(x.z); v[6] = bf16_lo(x.w); v[7] = bf16_hi(x.w);
+    };
+    auto use = [&](int row, const Row &x) {
+        float d[8], g[8], u[8];
+        if (F32) {
+            d[0] = __uint_as_float(x.d[0].x); d[1] = __uint_as_float(x.d[0].y);
+            d[2] = __uint_as_float(x.d[0].z); d[3] = __uint_as_float(x.d[0].w);
+            d[4] = __uint_as_float(x.d[ND - 1].x); d[5] = __uint_as_float(x.d[ND - 1].y);
+            d[6] = __uint_as_float(x.d[ND - 1].z); d[7] = __uint_as_float(x.d[ND - 1].w);
+        } else {
+            unpack(x.d[0], d);
+        }
+        if (ACT != 3) unpack(x.g, g);
+        if (GATED) unpack(x.u, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (GATED) {
+                const float s = lin_sigmoid(g[i]);
+                const float du = d[i] * g[i] * s;
+                d[i] = d[i] * u[i] * s * fmaf(g[i], 1.0f - s, 1.0f);
+                u[i] = du;
+                su[i] += du;
+            } else if (ACT == 1) {
+                d[i] *= lin_gelu_grad(g[i]);
+            } else if (ACT == 2) {
+                d[i] = g[i] > 0.0f ? d[i] : 0.0f;
+            }
+            sg[i] += d[i];
+        }
+        if (a.dz != nullptr) {
+            __nv_bfloat16 *o = a.dz + (size_t)row * cols + col;
+            *reinterpret_cast<uint4 *>(o) = lin_pack8(d);
+            if (GATED) *reinterpret_cast<uint4 *>(o + a.N) = lin_pack8(u);
+        }
+    };
     if (col < a.N) {
-        for (int row = blockIdx.y * a.rows + ty; row < r1; row += 8) {
-            float d[8], g[8], u[8];
-            if (a.dy_f32) {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.dy) +
-                                                                   (size_t)row * a.ldy + col);
-                const float4 x = p[0], y = p[1];
-                d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
-                d[4] = y.x; d[5] = y.y; d[6] = y.z; d[7] = y.w;
-            } else {
-                const uint4 x = *reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(a.dy) + (size_t)row * a.ldy + col);
-                d[0] = bf16_lo(x.x); d[1] = bf16_hi(x.x); d[2] = bf16_lo(x.y); d[3] = bf16_hi(x.y);
-                d[4] = bf16_lo(x.z); d[5] = bf16_hi(x.z); d[6] = bf16_lo(x.w); d[7] = bf16_hi(x.w);
-            }
-            if (a.act != 3) {
-                const __nv_bfloat16 *zr = a.z + (size_t)row * a.ldz + col;
-                const uint4 x = *reinterpret_cast<const uint4 *>(zr);
-                g[0] = bf16_lo(x.x); g[1] = bf16_hi(x.x); g[2] = bf16_lo(x.y); g[3] = bf16_hi(x.y);
-                g[4] = bf16_lo(x.z); g[5] = bf16_hi(x.z); g[6] = bf16_lo(x.w); g[7] = bf16_hi(x.w);
-                if (gated) {
-                    const uint4 y = *reinterpret_cast<const uint4 *>(zr + a.N);
-                    u[0] = bf16_lo(y.x); u[1] = bf16_hi(y.x); u[2] = bf16_lo(y.y); u[3] = bf16_hi(y.y);
-                    u[4] = bf16_lo(y.z); u[5] = bf16_hi(y.z); u[6] = bf16_lo(y.w); u[7] = bf16_hi(y.w);
-                }
-            }
-            if (gated) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float s = __fdividef(1.0f, 1.0f + __expf(-g[i]));
-                    const float dg = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-                    const float du = d[i] * g[i] * s;
-                    d[i] = dg;
-                    u[i] = du;
-                    sg[i] += dg;
-                    su[i] += du;
-                }
-                if (a.dz != nullptr) {
-                    __nv_bfloat16 *o = a.dz + (size_t)row * cols + col;
-                    *reinterpret_cast<uint4 *>(o) = lin_pack8(d);
-                    *reinterpret_cast<uint4 *>(o + a.N) = lin_pack8(u);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (a.act == 1) d[i] *= lin_gelu_grad(g[i]);
-                    if (a.act == 2) d[i] = g[i] > 0.0f ? d[i] : 0.0f;
-                    sg[i] += d[i];
-                }
-                if (a.dz != nullptr)
-                    *reinterpret_cast<uint4 *>(a.dz + (size_t)row * cols + col) = lin_pack8(d);
-            }
+        int row = blockIdx.y * a.rows + ty;
+        for (; row + 8 < r1; row += 16) {
+            Row x, y;
+            load(row, x);
+            load(row + 8, y);
+            use(row, x);
+            use(row + 8, y);
+        }
+        if (row < r1) {
+            Row x;
+            load(row, x);
+            use(row, x);
         }
     }
     if (a.part == nullptr) return;
@@ -924,7 +927,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
     }
     __syncthreads();
     // 256 gate (or plain) sums, then 256 up sums
-    for (int h = 0; h < (gated ? 2 : 1); ++h) {
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
         const int v = threadIdx.x >> 3, i = threadIdx.x & 7;
         const int c = (blockIdx.x * 32 + v) * 8 + i;
         if (c < a.N) {
@@ -936,16 +939,26 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
     }
 }
 
-// dbias[c] = the chunks' sums, in chunk order.
+// dbias[c] = the chunks' sums: eight threads a column take every eighth chunk in order, then the
+// eight in order. A block has 32 columns.
 __global__ void __launch_bounds__(256)
     linear_dbias_kernel(const float *__restrict__ part, int chunks, int cols, float *__restrict__ dbias)
 {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
+    __shared__ float red[8][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
     float s = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < chunks; ++i) s += part[(size_t)i * cols + c];
-    dbias[c] = s;
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = ty; i < chunks; i += 8) s += part[(size_t)i * cols + c];
+    }
+    red[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) t += red[y][tx];
+        dbias[c] = t;
+    }
 }
 
 } // namespace moe

@@ -153,30 +153,34 @@ struct LinearPlan {
     int splits; // 0: the persistent kernel; else blocks per cluster
 };
 
-// Tile width and k split by an estimate of the time of one launch, in SM cycles: a 64-value block of
-// k of a 128 x BN tile takes `step` cycles (measured); a persistent block pays start and last
-// epilogue once, a split one pays start, reduction and epilogue per tile. `wide`: 256-column tiles
-// are possible (not for fp32 outputs, whose sums are kept in registers).
+// Tile width and k split by an estimate of one launch's time in microseconds, from measurements at
+// 1 to 8192 rows: a 64-value block of k of a 128 x BN tile takes 0.30, 0.19, 0.165 (BN = 256, 128,
+// 64); a persistent launch pays start and last epilogue once (7.0, 5.5), a split one per tile, more of
+// it for more rows and splits. Measured, the choice against the best of the others: 1 x 4096 x 4096
+// (M x K x N) 9.7 (128 columns, 4 splits) / 10.4; 64 x 7168 x 2 * 2048 SwiGLU 16.1 (128, 4) / 19.2;
+// 128 x 4096 x 4096 12.8 (64, 2) / 14.5; 512 x 4096 x 4096 21.3 (128) / 22.4; 4096 x 7168 x 256 fp32
+// 22.2 (128, 2) / 25.9; 4096^3 104 (256) / 119. `wide`: 256-column tiles are possible (not for fp32
+// outputs, whose sums are kept in registers).
 LinearPlan plan_linear(int64_t M, int64_t n_out, bool gated, int64_t K, bool wide, int sms)
 {
     const int ft = g_linear_tile.load(), fs = g_linear_split.load();
     LinearPlan best{wide ? 256 : 128, 0};
     double tbest = 1e300;
     const int64_t mt = (M + lin::BM - 1) / lin::BM;
+    const double r = (M < lin::BM ? (double)M : (double)lin::BM) / 64.0;
     auto consider = [&](int bn, int s) {
         if (ft != 0 && (bn != ft || s != fs)) return;
         const int tc = gated ? bn / 2 : bn;
         const int64_t tiles = mt * ((n_out + tc - 1) / tc);
         const int64_t kb = (K + lin::bk(bn) - 1) / lin::bk(bn);
         if (s > kb) return;
-        const double step = bn == 256 ? 530.0 : 2.0 * (bn == 128 ? 300.0 : 260.0);
+        const double step = lin::sub(bn) * (bn == 256 ? 0.30 : bn == 128 ? 0.19 : 0.165);
         double t;
         if (s == 0) {
-            const int64_t waves = (tiles + sms - 1) / sms;
-            t = 4000.0 + waves * kb * step + 8.0 * bn;
+            t = (bn == 256 ? 7.0 : 5.5) + (double)((tiles + sms - 1) / sms) * kb * step;
         } else {
             const int64_t waves = (tiles * s + sms - 1) / sms;
-            t = waves * (4500.0 + ((kb + s - 1) / s) * step + 8.0 * bn + (s > 1 ? 800.0 + 100.0 * s : 0.0));
+            t = waves * (3.0 + 1.5 * r + (s - 1) * (0.5 + 0.47 * r) + (double)((kb + s - 1) / s) * step);
         }
         if (t < tbest) {
             tbest = t;
@@ -261,17 +265,6 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     a.splits = p.splits;
     a.a_rows = std::min(lin::BM, (a.M + 7) / 8 * 8);
     a.timeout_ns = g_timeout_ns.load();
-    a.a_ptr = A;
-    a.a_num = A_MN ? K : a.M;
-    a.a_row = 2 * (A_MN ? (int64_t)a.M : K);
-    a.a_ld = 2 * lda;
-    a.b_ptr = B;
-    a.b_num = B_MN ? K : b_cols;
-    a.b_row = 2 * (B_MN ? b_cols : K);
-    a.b_ld = 2 * ldb;
-    // few tiles that share their operands: latency, not rate, bounds their copies
-    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
-    a.ahead = a.m_tiles > 1 && tiles <= 2 * sms && a.a_num * a.a_row + a.b_num * a.b_row <= (32 << 20);
     CUtensorMap ta, tb;
     const bool ok = (A_MN ? make_map(&ta, A, (uint64_t)K, (uint64_t)a.M, (uint64_t)lda, 64)
                           : make_map(&ta, A, (uint64_t)a.M, (uint64_t)K, (uint64_t)lda, (uint32_t)a.a_rows)) &&
@@ -281,6 +274,26 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     if constexpr (!A_MN) // gradients of W are bf16
         if (promote) return launch_linear_plan<A_MN, B_MN, true>(p, ta, tb, a, sms, st);
     return launch_linear_plan<A_MN, B_MN, false>(p, ta, tb, a, sms, st);
+}
+
+template <int ACT> void launch_dz_of(const LinearDzArgs &a, dim3 grid, cudaStream_t st)
+{
+    if (a.dy_f32)
+        linear_dz_kernel<ACT, true><<<grid, 256, 0, st>>>(a);
+    else
+        linear_dz_kernel<ACT, false><<<grid, 256, 0, st>>>(a);
+}
+
+cudaError_t launch_dz(const LinearDzArgs &a, int act, int chunks, cudaStream_t st)
+{
+    const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)chunks);
+    switch (act) {
+    case MOE_ACT_SWIGLU: launch_dz_of<MOE_ACT_SWIGLU>(a, grid, st); break;
+    case MOE_ACT_GELU_TANH: launch_dz_of<MOE_ACT_GELU_TANH>(a, grid, st); break;
+    case MOE_ACT_RELU: launch_dz_of<MOE_ACT_RELU>(a, grid, st); break;
+    default: launch_dz_of<MOE_ACT_IDENTITY>(a, grid, st); break;
+    }
+    return cudaGetLastError();
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -469,12 +482,10 @@ moe_status moe_linear_backward(const moe_linear *p, const moe_bf16 *x, const moe
         z_.part = dbias == nullptr ? nullptr : L.chunks == 1 ? dbias : part;
         z_.M = p->M;
         z_.N = p->N;
-        z_.act = p->act;
         z_.rows = L.rows;
-        linear_dz_kernel<<<dim3((unsigned)((p->N + 255) / 256), (unsigned)L.chunks), 256, 0, st>>>(z_);
-        e = cudaGetLastError();
+        e = launch_dz(z_, p->act, L.chunks, st);
         if (e == cudaSuccess && dbias != nullptr && L.chunks > 1) {
-            linear_dbias_kernel<<<(unsigned)((d.cols + 255) / 256), 256, 0, st>>>(part, L.chunks,
+            linear_dbias_kernel<<<(unsigned)((d.cols + 31) / 32), 256, 0, st>>>(part, L.chunks,
                                                                                   (int)d.cols, dbias);
             e = cudaGetLastError();
         }
