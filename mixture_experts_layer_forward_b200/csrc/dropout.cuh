@@ -9,8 +9,9 @@
 // an even i. One counter serves eight elements, so a thread owns eight consecutive ones (one
 // 16-byte piece of bf16). p is a multiple of 2^-16 and the scale is its own, so the mean is kept.
 // Sums in fp32, one rounding. A dropped value is not multiplied, so an infinity or NaN there
-// does not pass. Bound by the bytes read and written: ten rounds are about 60 instructions for
-// eight elements.
+// does not pass. Bound by the bytes read and written (8192 x 4096 bf16 with a residual: 31 us, 6.4 TB/s,
+// the measured copy rate); without a residual the ten rounds, about 60 of 130 instructions for
+// eight elements, come close to the bytes (27 us against 21).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,26 +54,37 @@ __device__ __forceinline__ void dropout_bits(unsigned long long ctr, unsigned lo
     }
 }
 
-__device__ __forceinline__ float dropout_one(uint32_t u, uint32_t thr, float x, float scale, float r)
+// Eight consecutive elements as loaded: 16 bytes of bf16, 32 of fp32.
+template <typename DT> struct DropoutRaw {
+    uint4 p[sizeof(DT) / 2];
+    __device__ __forceinline__ void load(const DT *src)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(DT) / 2); ++i) p[i] = reinterpret_cast<const uint4 *>(src)[i];
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        if constexpr (sizeof(DT) == 2) {
+            v[0] = bf16_lo(p[0].x); v[1] = bf16_hi(p[0].x); v[2] = bf16_lo(p[0].y); v[3] = bf16_hi(p[0].y);
+            v[4] = bf16_lo(p[0].z); v[5] = bf16_hi(p[0].z); v[6] = bf16_lo(p[0].w); v[7] = bf16_hi(p[0].w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(p[i].x); v[4 * i + 1] = __uint_as_float(p[i].y);
+                v[4 * i + 2] = __uint_as_float(p[i].z); v[4 * i + 3] = __uint_as_float(p[i].w);
+            }
+        }
+    }
+};
+__device__ __forceinline__ uint32_t dropout_pack(float lo, float hi)
 {
-    return u >= thr ? fmaf(x, scale, r) : r;
-}
-
-__device__ __forceinline__ void dropout_load8(const __nv_bfloat16 *p, float (&v)[8])
-{
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
-    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
-}
-__device__ __forceinline__ void dropout_load8(const float *p, float (&v)[8])
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 __device__ __forceinline__ void dropout_store8(__nv_bfloat16 *p, const float (&v)[8])
 {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(p) = make_uint4(dropout_pack(v[0], v[1]), dropout_pack(v[2], v[3]),
+                                               dropout_pack(v[4], v[5]), dropout_pack(v[6], v[7]));
 }
 __device__ __forceinline__ void dropout_store8(float *p, const float (&v)[8])
 {
@@ -84,38 +96,73 @@ __device__ __forceinline__ float dropout_load1(const __nv_bfloat16 *p) { return 
 __device__ __forceinline__ void dropout_store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void dropout_store1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename DT>
-__global__ void __launch_bounds__(256) dropout_add_kernel(const DropoutArgs a)
+// v of group i: kept, scaled, plus r
+__device__ __forceinline__ void dropout_apply(const DropoutArgs &a, unsigned long long seed,
+                                              unsigned long long ctr, float (&v)[8], const float (&r)[8])
+{
+    uint32_t c[4];
+    dropout_bits(ctr, seed, c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = (c[q] & 0xffffu) >= a.thr ? fmaf(v[2 * q], a.scale, r[2 * q]) : r[2 * q];
+        v[2 * q + 1] = (c[q] >> 16) >= a.thr ? fmaf(v[2 * q + 1], a.scale, r[2 * q + 1]) : r[2 * q + 1];
+    }
+}
+
+// GROUPS groups of eight elements per thread and turn, their loads in flight together.
+template <typename DT, bool RES, int GROUPS>
+__global__ void __launch_bounds__(256) dropout_add_kernel(const __grid_constant__ DropoutArgs a)
 {
     const DT *x = static_cast<const DT *>(a.x), *res = static_cast<const DT *>(a.res);
     DT *y = static_cast<DT *>(a.y);
     const unsigned long long seed = a.rng[0], offset = a.rng[1];
-    const int64_t groups = (a.n + 7) / 8, stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < groups; i += stride) {
-        const bool whole = i * 8 + 8 <= a.n;
+    const int64_t whole = a.n / 8, stride = (int64_t)gridDim.x * 256;
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (; i + (GROUPS - 1) * stride < whole; i += GROUPS * stride) {
+        DropoutRaw<DT> xr[GROUPS], rr[GROUPS];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            xr[g].load(x + (i + g * stride) * 8);
+            if (RES) rr[g].load(res + (i + g * stride) * 8);
+        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            float v[8], r[8];
+            xr[g].values(v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) r[q] = 0.0f;
+            if (RES) rr[g].values(r);
+            dropout_apply(a, seed, offset + (unsigned long long)(i + g * stride), v, r);
+            dropout_store8(y + (i + g * stride) * 8, v);
+        }
+    }
+    for (; i < (a.n + 7) / 8; i += stride) { // the rest, and the elements behind the last whole group
         float v[8], r[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = r[q] = 0.0f;
-        if (whole) {
-            dropout_load8(x + i * 8, v);
-            if (res != nullptr) dropout_load8(res + i * 8, r);
+        if (i < whole) {
+            DropoutRaw<DT> xr, rr;
+            xr.load(x + i * 8);
+            if (RES) rr.load(res + i * 8);
+            xr.values(v);
+            if (RES) rr.values(r);
         } else {
-            for (int q = 0; q < 8; ++q)
-                if (i * 8 + q < a.n) {
-                    v[q] = dropout_load1(x + i * 8 + q);
-                    if (res != nullptr) r[q] = dropout_load1(res + i * 8 + q);
-                }
-        }
-        uint32_t c[4];
-        dropout_bits(offset + (unsigned long long)i, seed, c);
+#pragma unroll 1
+            for (int q = 0; q < (int)(a.n - i * 8); ++q) {
+                const float xv = dropout_load1(x + i * 8 + q), rv = RES ? dropout_load1(res + i * 8 + q) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            v[2 * q] = dropout_one(c[q] & 0xffffu, a.thr, v[2 * q], a.scale, r[2 * q]);
-            v[2 * q + 1] = dropout_one(c[q] >> 16, a.thr, v[2 * q + 1], a.scale, r[2 * q + 1]);
+                for (int j = 0; j < 8; ++j)
+                    if (j == q) {
+                        v[j] = xv;
+                        r[j] = rv;
+                    }
+            }
         }
-        if (whole) {
+        dropout_apply(a, seed, offset + (unsigned long long)i, v, r);
+        if (i < whole) {
             dropout_store8(y + i * 8, v);
         } else {
+#pragma unroll
             for (int q = 0; q < 8; ++q)
                 if (i * 8 + q < a.n) dropout_store1(y + i * 8 + q, v[q]);
         }

@@ -322,6 +322,25 @@ LinearBwdLayout linear_bwd_layout(const moe_linear *p, const LinearDims &d)
     return L;
 }
 
+// ---------------------------------------------------------------------------------------
+// dropout
+// ---------------------------------------------------------------------------------------
+
+// Groups per thread and turn: what keeps 64 to 96 bytes a thread in flight. Measured at 2^25
+// elements, 1 / 2 / 4 groups: bf16 with a residual 36.7 / 31.4 / 38.9 us, without 32.2 / 29.5 / 27.4;
+// fp32 61.9 / 66.1 / 64.7 and 44.4 / 51.6 / 55.6.
+template <typename DT> void launch_dropout(const DropoutArgs &a, cudaStream_t st)
+{
+    constexpr bool half = sizeof(DT) == 2;
+    const int sms = sm_count() > 0 ? sm_count() : 148;
+    const int64_t blocks = ((a.n + 7) / 8 + 255) / 256;
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8);
+    if (a.res != nullptr)
+        dropout_add_kernel<DT, true, half ? 2 : 1><<<grid, 256, 0, st>>>(a);
+    else
+        dropout_add_kernel<DT, false, half ? 4 : 1><<<grid, 256, 0, st>>>(a);
+}
+
 } // namespace
 
 extern "C" {
@@ -552,14 +571,11 @@ moe_status moe_dropout_add(int64_t n, int32_t dtype, int32_t drop, const uint64_
     a.n = n;
     a.thr = (uint32_t)drop;
     a.scale = a.thr < 65536u ? 65536.0f / (float)(65536u - a.thr) : 0.0f;
-    const int sms = sm_count() > 0 ? sm_count() : 148;
-    const int64_t blocks = ((n + 7) / 8 + 255) / 256;
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == MOE_DTYPE_F32)
-        dropout_add_kernel<float><<<grid, 256, 0, st>>>(a);
+        launch_dropout<float>(a, st);
     else
-        dropout_add_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+        launch_dropout<__nv_bfloat16>(a, st);
     return to_status(cudaGetLastError());
 }
 
