@@ -353,10 +353,10 @@ __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biase
 }
 
 // Threads per block and blocks per SM (the launch fills the SMs once).
-__host__ __device__ constexpr int sel_threads(int lpt, int ept) { return lpt == 32 && ept == 32 ? 128 : 256; }
+__host__ __device__ constexpr int sel_threads(int lpt, int ept) { return ept == 32 ? 128 : 256; }
 __host__ __device__ constexpr int sel_blocks(int lpt, int ept)
 {
-    return ept == 32 ? 3 : lpt == 8 || ept <= 4 ? 4 : ept == 16 ? 2 : 3;
+    return ept == 32 ? (lpt == 8 ? 6 : 3) : lpt == 8 || ept <= 4 ? 4 : ept == 16 ? 2 : 3;
 }
 // The bias in shared memory: lane i's EPT values, then (from 4) 4 more, so that 16-byte reads of
 // eight lanes meet no bank twice.
