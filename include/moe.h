@@ -553,7 +553,9 @@ MOE_API size_t moe_linear_workspace_size(const moe_linear *p);
 MOE_API size_t moe_linear_backward_workspace_size(const moe_linear *p);
 
 /* One launch: persistent tiles, or, where few tiles would leave SMs idle (small M, few columns),
- * tiles split along K over clusters of blocks that add their parts in a fixed order. */
+ * tiles split along K over clusters of blocks that add their parts in a fixed order. Launched in
+ * programmatic order: its blocks may be set up before the launch in front of it on the stream has
+ * ended, and read nothing before it has. */
 MOE_API moe_status moe_linear_forward(const moe_linear *p, const moe_bf16 *x, const moe_bf16 *W,
                                       const float *bias, const moe_bf16 *residual, void *y, moe_bf16 *z,
                                       void *ws, size_t ws_bytes, void *stream);
@@ -569,9 +571,10 @@ MOE_API moe_status moe_linear_backward(const moe_linear *p, const moe_bf16 *x, c
 
 /* Tile plan of later moe_linear_* launches (a test and tuning hook; not thread-safe): tile_n 0 (the
  * default) picks by an estimate; else tile_n columns with splits 0 (persistent; tile_n 128 or 256) or
- * splits 1, 2, 4 or 8 blocks per tile along K (tile_n 64 or 128). A plan that a problem cannot take
- * (SwiGLU with tile_n 64, more splits than 64-value blocks of K) falls back to tile_n 256, splits 0.
- * The plans differ in the order of the fp32 sums only. Returns 0, or -1 for an unknown plan. */
+ * splits 1, 2, 4 or 8 blocks per tile along K (tile_n 64 or 128). A product that cannot take the plan
+ * (SwiGLU with tile_n 64, more splits than blocks of 128 values of K, tile_n 256 with an fp32 output
+ * and K > 512) takes splits 0 with tile_n 256 (128 for such an output). The plans differ in the
+ * order of the fp32 sums only. Returns 0, or -1 for an unknown plan. */
 MOE_API int moe_set_linear_plan(int tile_n, int splits);
 
 /* Dropout with the residual: y_i = residual_i + (kept ? x_i / (1 - p) : 0) over n elements, with the

@@ -102,6 +102,28 @@ def test_routed_layer_reports_bad_ids(T):
     assert torch.isfinite(dW1.float()).all() and torch.isfinite(dx.float()).all()
 
 
+@pytest.mark.parametrize("T,E", [(300, 16), (5, 16), (700, 8)])
+def test_routed_layer_reports_an_expert_given_twice(T, E):
+    """The call reports it and leaves the other tokens' rows as they should be."""
+    cfg = synth.LayerConfig("twice", T=T, H=128, F=128, E=E, k=2)
+    inp = synth.make_inputs(cfg, seed=2, device="cuda")
+    p = moe.Problem.from_config(cfg)
+    idx = torch.stack([torch.randperm(E)[:2] for _ in range(T)]).to(I32).cuda()
+    w = torch.rand(T, 2, device="cuda")
+    ws = zeros(moe.moe_backward_workspace_size(p))
+    ok, out, dx = empty(T, 128), empty(T, 128), empty(T, 128)
+    dw, dW1, dW2 = empty(T, 2, dtype=F32), torch.empty_like(inp["W1"]), torch.empty_like(inp["W2"])
+    moe.moe_forward_routed(p, inp["x"], idx, w, inp["W1"], inp["W2"], ok, ws)
+    idx[2, 1] = idx[2, 0]
+    moe.moe_forward_routed(p, inp["x"], idx, w, inp["W1"], inp["W2"], out, ws)
+    assert moe.moe_get_device_status(ws) == -6
+    keep = [t for t in range(T) if t != 2]
+    assert torch.equal(out[keep], ok[keep])
+    moe.moe_backward_routed(p, inp["x"], idx, w, inp["W1"], inp["W2"], ok, dx, dw, dW1, dW2, ws)
+    assert moe.moe_get_device_status(ws) == -6
+    assert torch.isfinite(dx[keep].float()).all()
+
+
 def test_no_tokens():
     p = moe.Problem.make(0, 128, 128, 16, 2)
     W1, W2 = empty(16, 128, 256), empty(16, 128, 128)
