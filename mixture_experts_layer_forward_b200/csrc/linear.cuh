@@ -842,7 +842,7 @@ struct LinearDzArgs {
 // thread, their loads in flight together); the sums over a chunk's rows run in fp32 in a fixed order
 // (rows of one thread, then the eight threads). Bound by the bytes of dy, z and dz.
 template <int ACT, bool F32>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ LinearDzArgs a)
+__global__ void __launch_bounds__(256, ACT == 0 ? 3 : 5) linear_dz_kernel(const __grid_constant__ LinearDzArgs a)
 {
     constexpr bool GATED = ACT == 0;
     constexpr int ND = F32 ? 2 : 1; // 16-byte pieces of eight dy
