@@ -177,7 +177,10 @@ LinearPlan plan_linear(int64_t M, int64_t n_out, bool gated, int64_t K, bool wid
         const double step = lin::sub(bn) * (bn == 256 ? 0.30 : bn == 128 ? 0.19 : 0.165);
         double t;
         if (s == 0) {
-            t = (bn == 256 ? 7.0 : 5.5) + (double)((tiles + sms - 1) / sms) * kb * step;
+            const int64_t rest = tiles % sms;
+            double waves = (double)((tiles + sms - 1) / sms);
+            if (bn == 256 && tiles > sms && rest > 0 && 2 * rest <= sms) waves -= 0.4; // the last in halves
+            t = (bn == 256 ? 7.0 : 5.5) + waves * kb * step;
         } else {
             const int64_t waves = (tiles * s + sms - 1) / sms;
             t = waves * (3.0 + 1.5 * r + (s - 1) * (0.5 + 0.47 * r) + (double)((kb + s - 1) / s) * step);
@@ -265,11 +268,15 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     a.splits = p.splits;
     a.a_rows = std::min(lin::BM, (a.M + 7) / 8 * 8);
     a.timeout_ns = g_timeout_ns.load();
+    // a last wave of at most half the SMs' tiles is worked in halves
+    const int tiles = a.m_tiles * a.n_tiles, rest = tiles % sms;
+    a.full = tiles > sms && 2 * rest <= sms ? tiles - rest : tiles;
     CUtensorMap ta, tb;
     const bool ok = (A_MN ? make_map(&ta, A, (uint64_t)K, (uint64_t)a.M, (uint64_t)lda, 64)
                           : make_map(&ta, A, (uint64_t)a.M, (uint64_t)K, (uint64_t)lda, (uint32_t)a.a_rows)) &&
                     (B_MN ? make_map(&tb, B, (uint64_t)K, (uint64_t)b_cols, (uint64_t)ldb, 64)
-                          : make_map(&tb, B, (uint64_t)b_cols, (uint64_t)K, (uint64_t)ldb, (uint32_t)tc));
+                          : make_map(&tb, B, (uint64_t)b_cols, (uint64_t)K, (uint64_t)ldb,
+                                     p.bn == 256 ? 64u : (uint32_t)tc));
     if (!ok) return cudaErrorInvalidValue;
     if constexpr (!A_MN) // gradients of W are bf16
         if (promote) return launch_linear_plan<A_MN, B_MN, true>(p, ta, tb, a, sms, st);

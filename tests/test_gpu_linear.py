@@ -332,3 +332,16 @@ def test_larger_sizes(M, K, N, act):
     p = moe.Linear.make(M, N, K, act=act, out_dtype=out)
     check_forward(p, d, True, act != IDENT, True)
     check_backward(p, d)
+
+
+@pytest.mark.parametrize("nk", [False, True])
+@pytest.mark.parametrize("M,K,N,act", [(1304, 200, 3592, GELU), (1304, 72, 1800, SWIGLU), (1304, 3592, 136, IDENT),
+                                       (72, 1304, 3592, IDENT), (1300, 264, 3712, RELU)])
+def test_last_wave_of_tiles(M, K, N, act, nk):
+    """More 256-column tiles than SMs, and few in the last wave (165 of them on 148 SMs), whose last
+    columns end just behind a tile's first half, or just inside it."""
+    moe.moe_set_linear_plan(256, 0)
+    d = make(M, K, N, act, nk, 31)
+    p = moe.Linear.make(M, N, K, act=act, w_layout=moe.W_NK if nk else moe.W_KN)
+    check_forward(p, d, True, True, True)
+    check_backward(p, d)
