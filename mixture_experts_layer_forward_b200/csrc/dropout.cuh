@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "order.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -113,6 +114,8 @@ __device__ __forceinline__ void dropout_apply(const DropoutArgs &a, unsigned lon
 template <typename DT, bool RES, int GROUPS>
 __global__ void __launch_bounds__(256) dropout_add_kernel(const __grid_constant__ DropoutArgs a)
 {
+    order_launch_dependents();
+    order_wait();
     const DT *x = static_cast<const DT *>(a.x), *res = static_cast<const DT *>(a.res);
     DT *y = static_cast<DT *>(a.y);
     const unsigned long long seed = a.rng[0], offset = a.rng[1];

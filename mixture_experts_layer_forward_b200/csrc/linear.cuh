@@ -27,6 +27,7 @@
 // timeout, waits for its copies and products in flight, frees its TMEM and leaves.
 #pragma once
 
+#include "order.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -250,12 +251,6 @@ template <int BN> __device__ __forceinline__ LinItem lin_item(int w, const Linea
     return it;
 }
 
-// Programmatic launch order: the next call's blocks may be set up from here on; and what earlier
-// launches wrote is visible after the wait (every thread waits, so a call never ends before the
-// ones in front of it).
-__device__ __forceinline__ void lin_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void lin_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The barriers and the two pipeline roles, shared by both kernels.
 template <int BN, bool A_MN, bool B_MN> struct LinPipe {
     static constexpr int STAGES = lin::stages(BN);
@@ -444,7 +439,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + lin::num_bars(BN));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    lin_launch_dependents();
+    order_launch_dependents();
     if (threadIdx.x == 0) {
         p.init_bars(true);
         *abort_flag = 0;
@@ -462,7 +457,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int total = BN == 256 ? 2 * a.m_tiles * a.n_tiles - a.full : a.m_tiles * a.n_tiles;
     const int tc = a.act == 0 ? BN / 2 : BN;
     const int run = PROMOTE ? lin::PROMOTE_K / lin::bk(BN) : a.k_blocks;
-    lin_dependency_wait();
+    order_wait();
     if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
         a.status[0] = DEV_OK;
         a.status[1] = 0;
@@ -683,7 +678,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.splits;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-    lin_launch_dependents();
+    order_launch_dependents();
     if (threadIdx.x == 0) {
         p.init_bars(true);
         *abort_flag = 0;
@@ -707,7 +702,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int rows = min(lin::BM, a.M - mt * lin::BM);
     float *park = reinterpret_cast<float *>(p.smem);
     const LinPark lay(BN, S, gated);
-    lin_dependency_wait();
+    order_wait();
     if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
         a.status[0] = DEV_OK;
         a.status[1] = 0;
@@ -873,6 +868,8 @@ __global__ void __launch_bounds__(256, ACT == 0 ? 3 : 5) linear_dz_kernel(const 
 {
     constexpr bool GATED = ACT == 0;
     constexpr int ND = F32 ? 2 : 1; // 16-byte pieces of eight dy
+    order_launch_dependents();
+    order_wait();
     __shared__ float red[8][32][17];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int col = (blockIdx.x * 32 + tx) * 8;
@@ -966,25 +963,33 @@ __global__ void __launch_bounds__(256, ACT == 0 ? 3 : 5) linear_dz_kernel(const 
     }
 }
 
+struct LinearDbiasArgs {
+    const float *part; // [chunks, cols]
+    float *dbias;      // [cols]
+    int chunks, cols;
+};
+
 // dbias[c] = the chunks' sums: eight threads a column take every eighth chunk in order, then the
 // eight in order. A block has 32 columns.
 __global__ void __launch_bounds__(256)
-    linear_dbias_kernel(const float *__restrict__ part, int chunks, int cols, float *__restrict__ dbias)
+    linear_dbias_kernel(const __grid_constant__ LinearDbiasArgs a)
 {
+    order_launch_dependents();
+    order_wait();
     __shared__ float red[8][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
     float s = 0.0f;
-    if (c < cols) {
+    if (c < a.cols) {
 #pragma unroll 8
-        for (int i = ty; i < chunks; i += 8) s += part[(size_t)i * cols + c];
+        for (int i = ty; i < a.chunks; i += 8) s += a.part[(size_t)i * a.cols + c];
     }
     red[ty][tx] = s;
     __syncthreads();
-    if (ty == 0 && c < cols) {
+    if (ty == 0 && c < a.cols) {
         float t = 0.0f;
 #pragma unroll
         for (int y = 0; y < 8; ++y) t += red[y][tx];
-        dbias[c] = t;
+        a.dbias[c] = t;
     }
 }
 

@@ -18,6 +18,23 @@ namespace {
 
 using namespace moe;
 
+// A launch in programmatic order (order.cuh).
+template <typename A>
+cudaError_t launch_ordered(void (*kern)(A), dim3 grid, int threads, size_t smem, cudaStream_t st, const A &args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
 // ---------------------------------------------------------------------------------------
 // routing by scores
 // ---------------------------------------------------------------------------------------
@@ -283,24 +300,21 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     return launch_linear_plan<A_MN, B_MN, false>(p, ta, tb, a, sms, st);
 }
 
-template <int ACT> void launch_dz_of(const LinearDzArgs &a, dim3 grid, cudaStream_t st)
+template <int ACT> cudaError_t launch_dz_of(const LinearDzArgs &a, dim3 grid, cudaStream_t st)
 {
-    if (a.dy_f32)
-        linear_dz_kernel<ACT, true><<<grid, 256, 0, st>>>(a);
-    else
-        linear_dz_kernel<ACT, false><<<grid, 256, 0, st>>>(a);
+    return a.dy_f32 ? launch_ordered(linear_dz_kernel<ACT, true>, grid, 256, 0, st, a)
+                    : launch_ordered(linear_dz_kernel<ACT, false>, grid, 256, 0, st, a);
 }
 
 cudaError_t launch_dz(const LinearDzArgs &a, int act, int chunks, cudaStream_t st)
 {
     const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)chunks);
     switch (act) {
-    case MOE_ACT_SWIGLU: launch_dz_of<MOE_ACT_SWIGLU>(a, grid, st); break;
-    case MOE_ACT_GELU_TANH: launch_dz_of<MOE_ACT_GELU_TANH>(a, grid, st); break;
-    case MOE_ACT_RELU: launch_dz_of<MOE_ACT_RELU>(a, grid, st); break;
-    default: launch_dz_of<MOE_ACT_IDENTITY>(a, grid, st); break;
+    case MOE_ACT_SWIGLU: return launch_dz_of<MOE_ACT_SWIGLU>(a, grid, st);
+    case MOE_ACT_GELU_TANH: return launch_dz_of<MOE_ACT_GELU_TANH>(a, grid, st);
+    case MOE_ACT_RELU: return launch_dz_of<MOE_ACT_RELU>(a, grid, st);
+    default: return launch_dz_of<MOE_ACT_IDENTITY>(a, grid, st);
     }
-    return cudaGetLastError();
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -337,16 +351,14 @@ LinearBwdLayout linear_bwd_layout(const moe_linear *p, const LinearDims &d)
 // Groups per thread and turn: what keeps 64 to 96 bytes a thread in flight. Measured at 2^25
 // elements, 1 / 2 / 4 groups: bf16 with a residual 36.7 / 31.4 / 38.9 us, without 32.2 / 29.5 / 27.4;
 // fp32 61.9 / 66.1 / 64.7 and 44.4 / 51.6 / 55.6.
-template <typename DT> void launch_dropout(const DropoutArgs &a, cudaStream_t st)
+template <typename DT> cudaError_t launch_dropout(const DropoutArgs &a, cudaStream_t st)
 {
     constexpr bool half = sizeof(DT) == 2;
     const int sms = sm_count() > 0 ? sm_count() : 148;
     const int64_t blocks = ((a.n + 7) / 8 + 255) / 256;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8);
-    if (a.res != nullptr)
-        dropout_add_kernel<DT, true, half ? 2 : 1><<<grid, 256, 0, st>>>(a);
-    else
-        dropout_add_kernel<DT, false, half ? 4 : 1><<<grid, 256, 0, st>>>(a);
+    return a.res != nullptr ? launch_ordered(dropout_add_kernel<DT, true, half ? 2 : 1>, grid, 256, 0, st, a)
+                            : launch_ordered(dropout_add_kernel<DT, false, half ? 4 : 1>, grid, 256, 0, st, a);
 }
 
 } // namespace
@@ -512,9 +524,8 @@ moe_status moe_linear_backward(const moe_linear *p, const moe_bf16 *x, const moe
         z_.rows = L.rows;
         e = launch_dz(z_, p->act, L.chunks, st);
         if (e == cudaSuccess && dbias != nullptr && L.chunks > 1) {
-            linear_dbias_kernel<<<(unsigned)((d.cols + 31) / 32), 256, 0, st>>>(part, L.chunks,
-                                                                                  (int)d.cols, dbias);
-            e = cudaGetLastError();
+            e = launch_ordered(linear_dbias_kernel, dim3((unsigned)((d.cols + 31) / 32)), 256, 0, st,
+                               LinearDbiasArgs{part, dbias, L.chunks, (int)d.cols});
         }
     }
     if (!gemms) {
@@ -580,11 +591,8 @@ moe_status moe_dropout_add(int64_t n, int32_t dtype, int32_t drop, const uint64_
     a.thr = (uint32_t)drop;
     a.scale = a.thr < 65536u ? 65536.0f / (float)(65536u - a.thr) : 0.0f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == MOE_DTYPE_F32)
-        launch_dropout<float>(a, st);
-    else
-        launch_dropout<__nv_bfloat16>(a, st);
-    return to_status(cudaGetLastError());
+    return to_status(dtype == MOE_DTYPE_F32 ? launch_dropout<float>(a, st)
+                                            : launch_dropout<__nv_bfloat16>(a, st));
 }
 
 moe_status moe_dropout_add_backward(int64_t n, int32_t dtype, int32_t drop, const uint64_t *rng,
