@@ -146,3 +146,15 @@ def test_share_kept_and_independence():
     for share, p in ((ka.mean(), 0.75), (kb.mean(), 0.75), ((ka * kb).mean(), 0.5625),
                      ((ka[1:] * ka[:-1]).mean(), 0.5625)):
         assert abs(float(share) - p) < 6 * (p * (1 - p) / n) ** 0.5 * 2
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: the last ones are those of a small call at their counters."""
+    n, m = (1 << 32) + 19, 4096 + 3
+    x = torch.full((n,), 1.0, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    moe.moe_dropout_add(x, x, y, 0.25, state(5, 7))
+    start = (n - m) // 8 * 8
+    part = torch.empty(n - start, dtype=torch.bfloat16, device="cuda")
+    moe.moe_dropout_add(x[start:], x[start:], part, 0.25, state(5, 7 + start // 8))
+    assert torch.equal(y[start:], part)

@@ -345,3 +345,28 @@ def test_last_wave_of_tiles(M, K, N, act, nk):
     p = moe.Linear.make(M, N, K, act=act, w_layout=moe.W_NK if nk else moe.W_KN)
     check_forward(p, d, True, True, True)
     check_backward(p, d)
+
+
+def test_offsets_past_32_bits():
+    """Outputs, residual, saved z and gradients of more than 2^31 elements: the last rows equal those of
+    a small call."""
+    M, K, N, m = 70016, 64, 32768, 128
+    g = torch.Generator().manual_seed(3)
+    W = (torch.randn(K, N, generator=g) / 8).to(BF).cuda()
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    x[-m:] = torch.randn(m, K, generator=g).to(BF).cuda()
+    res = torch.ones(M, N, dtype=BF, device="cuda")
+    p, q = moe.Linear.make(M, N, K, act=GELU), moe.Linear.make(m, N, K, act=GELU)
+    moe.moe_set_linear_plan(256, 0)
+    ws = torch.empty(moe.moe_linear_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
+    y, z = (torch.empty(M, N, dtype=BF, device="cuda") for _ in range(2))
+    moe.moe_linear_forward(p, x, W, None, res, y, ws, z=z)
+    ys, zs = (torch.empty(m, N, dtype=BF, device="cuda") for _ in range(2))
+    moe.moe_linear_forward(q, x[-m:], W, None, res[-m:], ys, ws, z=zs)
+    assert moe.moe_get_device_status(ws) == 0
+    assert torch.equal(y[-m:], ys) and torch.equal(z[-m:], zs) and (y[:m] == 1).all()
+    dx, dxs = torch.empty_like(x), torch.empty(m, K, dtype=BF, device="cuda")
+    moe.moe_linear_backward(p, x, W, z, res, dx, None, None, ws)
+    moe.moe_linear_backward(q, x[-m:], W, zs, res[-m:], dxs, None, None, ws)
+    assert moe.moe_get_device_status(ws) == 0
+    assert torch.equal(dx[-m:], dxs)

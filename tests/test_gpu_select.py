@@ -425,3 +425,24 @@ def test_large_batches(E, k, G, keep, score):
         a = at.numpy()
         assert np.array_equal(gi, ri[a]), (i, np.argwhere(gi != ri[a])[:4])
         assert np.all(np.abs(gw - rw[a]) <= tol[a])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 logits: the last rows are the ones that a small call gives."""
+    T, E, k = (1 << 22) + 3, 1024, 4
+    g = torch.Generator().manual_seed(2)
+    tail = torch.randn(64, E, generator=g).to(torch.bfloat16).cuda()
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    logits[:, 5] = 1.0
+    logits[-64:] = tail
+    idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    moe.moe_route_select(moe.Select.make(T, E, k, score=moe.SCORE_SOFTMAX), logits, None, idx, w)
+    si, sw = torch.empty(64, k, dtype=torch.int32, device="cuda"), torch.empty(64, k, device="cuda")
+    s = moe.Select.make(64, E, k, score=moe.SCORE_SOFTMAX)
+    moe.moe_route_select(s, tail, None, si, sw)
+    assert torch.equal(idx[-64:], si) and torch.equal(w[-64:], sw)
+    assert (idx[:-64] == torch.tensor([5, 0, 1, 2], device="cuda")).all()
+    d, sd = torch.empty_like(logits), torch.empty_like(tail)
+    moe.moe_route_select_backward(moe.Select.make(T, E, k, score=moe.SCORE_SOFTMAX), logits, idx, w, d)
+    moe.moe_route_select_backward(s, tail, si, sw, sd)
+    assert torch.equal(d[-64:], sd)
