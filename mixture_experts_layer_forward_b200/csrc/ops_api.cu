@@ -426,7 +426,7 @@ moe_status moe_route_select_backward(const moe_select *s, const void *logits, co
     a.renorm = s->renorm != 0;
     a.scale = s->scale;
     a.vec = aligned16(dlogits) && (int64_t)s->E * b % 16 == 0;
-    const unsigned grid = (unsigned)((a.T + 7) / 8);
+    const unsigned grid = (unsigned)(((int64_t)a.T + 7) / 8);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s->dtype == MOE_DTYPE_F32)
         route_select_bwd_kernel<float><<<grid, 256, 0, st>>>(a);

@@ -446,3 +446,22 @@ def test_offsets_past_32_bits():
     moe.moe_route_select_backward(moe.Select.make(T, E, k, score=moe.SCORE_SOFTMAX), logits, idx, w, d)
     moe.moe_route_select_backward(s, tail, si, sw, sd)
     assert torch.equal(d[-64:], sd)
+
+
+def test_the_largest_row_count():
+    """T = 2^31 - 1 with 5 rows in use: the rows behind them are not read or written, so the buffers
+    hold those 5 rows."""
+    lib, T, n = moe._native.library(), 2**31 - 1, 5
+    l, b = draw(n, 16, 21)
+    small, s = moe.Select.make(n, 16, 3), moe.Select.make(T, 16, 3)
+    ref_idx, ref_w = check(small, l, b)
+    cnt = torch.tensor([n], dtype=torch.int32, device="cuda")
+    lc, bc, dw = l.cuda(), b.cuda(), torch.arange(15.0, device="cuda").reshape(n, 3)
+    idx, w = torch.empty(n, 3, dtype=torch.int32, device="cuda"), torch.empty(n, 3, device="cuda")
+    d, ref_d = torch.full((n, 16), 7.0, device="cuda"), torch.empty(n, 16, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.moe_route_select(s, lc.data_ptr(), bc.data_ptr(), idx.data_ptr(), w.data_ptr(), cnt.data_ptr(), st) == 0
+    assert lib.moe_route_select_backward(s, lc.data_ptr(), idx.data_ptr(), dw.data_ptr(), d.data_ptr(),
+                                         cnt.data_ptr(), st) == 0
+    moe.moe_route_select_backward(small, lc, ref_idx, dw, ref_d)
+    assert torch.equal(idx, ref_idx) and torch.equal(w, ref_w) and torch.equal(d, ref_d)
