@@ -441,7 +441,14 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
         } else {
             sel_load_row(a, row, e0, v);
         }
-        if (!(BIASED && a.sigmoid)) { // NaN: masked (a sigmoid and the test of its key need no clamp)
+        if constexpr (BIASED) {
+            // Every finite logit is live, the lowest too, and its bias may win: only -inf and NaN are
+            // masked (a sigmoid and the test of its key need no clamp)
+            if (!a.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(v[i], -INFINITY), SEL_FAR);
+            }
+        } else { // the order of the logits: below -SEL_EDGE sel_exact settles what is live
 #pragma unroll
             for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(v[i], -SEL_FAR), SEL_FAR);
         }
@@ -453,7 +460,9 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
             m = v[0];
 #pragma unroll
             for (int i = 1; i < EPT; ++i) m = fmaxf(m, v[i]);
-            m = sel_max_of<LPT>(m);
+            // no live logit is below the floor, so the largest adds 1 and the sum is 0 only where every
+            // expert is masked: no key is NaN
+            m = fmaxf(sel_max_of<LPT>(m), -FLT_MAX);
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPT; ++i) s += sel_ex2((v[i] - m) * SEL_LOG2E);
@@ -476,11 +485,11 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
             if (a.sigmoid) {
 #pragma unroll
                 for (int i = 0; i < EPT; ++i)
-                    v[i] = v[i] > -SEL_EDGE ? sel_rcp(1.0f + sel_ex2(v[i] * -SEL_LOG2E)) + b[i] : -SEL_FAR;
+                    v[i] = v[i] > -INFINITY ? sel_rcp(1.0f + sel_ex2(v[i] * -SEL_LOG2E)) + b[i] : -SEL_FAR;
             } else {
 #pragma unroll
                 for (int i = 0; i < EPT; ++i)
-                    v[i] = v[i] > -SEL_EDGE ? sel_ex2((v[i] - m) * SEL_LOG2E) * inv + b[i] : -SEL_FAR;
+                    v[i] = v[i] > -INFINITY ? sel_ex2((v[i] - m) * SEL_LOG2E) * inv + b[i] : -SEL_FAR;
             }
         }
         float tol = a.sigmoid ? SEL_TOL_SIGMOID : SEL_TOL_SOFTMAX * inv;

@@ -465,3 +465,42 @@ def test_the_largest_row_count():
                                          cnt.data_ptr(), st) == 0
     moe.moe_route_select_backward(small, lc, ref_idx, dw, ref_d)
     assert torch.equal(idx, ref_idx) and torch.equal(w, ref_w) and torch.equal(d, ref_d)
+
+
+def check_rows(rows, E, k, bias, seed=0, **kw):
+    """The rows as a small batch, and many times over, in another order, in a batch that puts several
+    tokens on a warp: both against the reference."""
+    n, T = len(rows), 8203
+    check(moe.Select.make(n, E, k, **kw), rows, bias)
+    small, big = moe.Select.make(n, E, k, **kw), moe.Select.make(T, E, k, **kw)
+    l = rows.float().numpy()
+    ri, rw = ref_select(small, l, None if bias is None else bias.numpy())
+    at = torch.randperm(T, generator=torch.Generator().manual_seed(seed)) % n
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -7.0, device="cuda")
+    moe.moe_route_select(big, rows[at].cuda(), None if bias is None else bias.cuda(), idx, w)
+    gi, gw, a = idx.cpu().numpy(), w.cpu().numpy().astype(np.float64), at.numpy()
+    assert np.array_equal(gi, ri[a]), np.argwhere(gi != ri[a])[:4]
+    assert np.all(np.abs(gw - rw[a]) <= weight_tol(small, l, rw)[a])
+
+
+LOW = -3.3e38    # finite in bf16 and fp32, and below any key that 32 bits carry through a sum
+EDGE_SHAPES = [(8, 1, 1, 1), (8, 2, 2, 1), (60, 2, 5, 2), (64, 3, 1, 1), (64, 8, 8, 3), (256, 8, 8, 4),
+               (400, 6, 8, 2)]
+
+
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k,G,keep", EDGE_SHAPES)
+def test_live_logits_of_the_lowest_value_with_a_bias(E, k, G, keep, dtype, score):
+    """Only -inf and NaN mask: an expert at the type's lowest finite value has score 0 and is selected
+    where its bias wins."""
+    g = torch.Generator().manual_seed(E + k)
+    l, b = draw(48, E, E, dtype)
+    b[torch.rand(E, generator=g) < 0.3] = 1.5        # larger than any other key where the score is small
+    for v, share in ((torch.finfo(dtype).min, 0.3), (LOW, 0.1), (-math.inf, 0.1)):
+        l[torch.rand(48, E, generator=g) < share] = v
+    l[0] = l[0].clamp(min=-4)
+    l[0, 0], b[0] = torch.finfo(dtype).min, 1.5
+    for sum2 in (moe.GROUP_MAX, moe.GROUP_SUM2):
+        check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=sum2)
