@@ -56,8 +56,12 @@ constexpr float SEL_TOL_KEY = 2.384185791015625e-7f;   // 2^-22, times the key
 constexpr float SEL_TOL_ZERO = 1.0e-40f;               // a place in a zero or denormal key
 __host__ __device__ constexpr float SEL_PLACE(int ept) { return ept * 1.1920928955078125e-7f; } // EPT 2^-23
 // Masked or excluded experts' key, and the clamp of the others; a winner at or beyond SEL_EDGE
-// (also a lane whose sorted keys ran out) sends the token to sel_exact.
+// (also a lane whose sorted keys ran out) sends the token to sel_exact. A live expert's key is clamped
+// at -SEL_LOW where a group's sum has to tell it from a masked one: keys below -SEL_NONE (places and
+// ids in their lowest bits included) are no experts.
 constexpr float SEL_FAR = 3.0e38f;
+constexpr float SEL_NONE = 2.97e38f;
+constexpr float SEL_LOW = 2.95e38f;
 constexpr float SEL_EDGE = 2.9e38f;
 
 struct SelectArgs {
@@ -326,8 +330,12 @@ __device__ __forceinline__ void sel_load_row(const SelectArgs &a, const LT *row,
     }
 }
 
-// a finite bias: beyond SEL_EDGE sel_exact decides (a NaN bias counts as -inf)
-__device__ __forceinline__ float sel_bias(float b) { return fminf(fmaxf(b, -SEL_FAR), SEL_FAR); }
+// a finite bias: beyond SEL_EDGE sel_exact decides; -inf (and NaN, which counts as it) is as good as
+// a mask, but a finite one is not: it brings its group's sum down
+__device__ __forceinline__ float sel_bias(float b)
+{
+    return b > -INFINITY ? fminf(fmaxf(b, -SEL_LOW), SEL_FAR) : -SEL_FAR;
+}
 
 // the expert id that an IDS key carries
 __device__ __forceinline__ int sel_id(float key)
@@ -342,13 +350,20 @@ __device__ __forceinline__ float sel_score(int sigmoid, float l, float m, float 
     return sigmoid ? sel_rcp(1.0f + sel_ex2(l * -SEL_LOG2E)) : sel_ex2((l - m) * SEL_LOG2E) * inv;
 }
 
-// A group's value from its two largest keys (SEL_FAR: none). Without a bias the keys are logits and
-// a sum is formed of their scores (the order is the same).
+// A group's value from its two largest keys (-SEL_FAR: none). Without a bias the keys are logits and
+// a sum is formed of their scores (the order is the same). A sum with a live expert's key at -SEL_LOW
+// is lost, as that key is: -SEL_LOW. (One with a key beyond SEL_EDGE is that key, which wins and sends
+// the token to sel_exact.)
 __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biased, float v1, float v2,
                                                  float m, float inv)
 {
-    if (!a.sum2 || !(v1 > -SEL_EDGE)) return v1;
-    if (biased) return v2 > -SEL_EDGE ? v1 + v2 : v1;
+    if (!a.sum2 || !(v1 > -SEL_NONE)) return v1;
+    if (biased) {
+        const bool two = v2 > -SEL_NONE;
+        if (!((two ? v2 : v1) > -SEL_EDGE)) return v1 >= SEL_EDGE ? v1 : -SEL_LOW;
+        return two && v1 < SEL_EDGE ? v1 + v2 : v1;
+    }
+    if (!(v1 > -SEL_EDGE)) return v1;
     return sel_score(a.sigmoid, v1, m, inv) + (v2 > -SEL_EDGE ? sel_score(a.sigmoid, v2, m, inv) : 0.0f);
 }
 
@@ -519,7 +534,8 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
             const uint32_t stay = __ballot_sync(0xffffffffu, st);
             const float lo = sel_min_of<LPT>(st ? gv : SEL_FAR);
             const float hi = sel_max_of<LPT>(!st && lane < a.groups ? gv : -SEL_FAR);
-            if ((BIASED || sums) && hi > -SEL_FAR && !(lo - hi > 2.0f * tol + SEL_TOL_KEY * (fabsf(lo) + fabsf(hi))))
+            // (a lost group that stays while another lost one does not is as close as can be)
+            if ((BIASED || sums) && hi > -SEL_NONE && !(lo - hi > 2.0f * tol + SEL_TOL_KEY * (fabsf(lo) + fabsf(hi))))
                 bad = true;
 #pragma unroll
             for (int i = 0; i < EPT; ++i)
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
             bool st = in && rank < a.keep;
             if (!EXACT || sums) {
                 const float lo = sel_min_of<LPT>(st ? gv : SEL_FAR), hi = sel_max_of<LPT>(in && !st ? gv : -SEL_FAR);
-                const bool close = hi > -SEL_EDGE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) +
+                const bool close = hi > -SEL_NONE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) +
                                                                      TOL_KEY * (fabsf(lo) + fabsf(hi)) + SEL_TOL_ZERO);
                 if (__any_sync(0xffffffffu, close)) {
                     // the groups' values again in 64 bits, from each lane's two largest (which are its two
@@ -587,7 +603,7 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
                     const bool sure = !(third > -SEL_EDGE) ||
                                       second - third > tol + TOL_KEY * (fabsf(second) + fabsf(third)) + SEL_TOL_ZERO;
                     auto value = [&](float key) -> double {
-                        if (!(key > -SEL_EDGE)) return -INFINITY;
+                        if (!(key > -SEL_NONE)) return -INFINITY;
                         const int e = IDS ? sel_id(key) : e0 + (EPT > 1 ? (int)(__float_as_uint(key) & (uint32_t)(EPT - 1)) : 0);
                         const float l = sel_load(row + e);
                         return BIASED || sums ? sel_value64(l, BIASED ? a.bias[e] : 0.0f) : (double)l;

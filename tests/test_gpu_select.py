@@ -504,3 +504,22 @@ def test_live_logits_of_the_lowest_value_with_a_bias(E, k, G, keep, dtype, score
     l[0, 0], b[0] = torch.finfo(dtype).min, 1.5
     for sum2 in (moe.GROUP_MAX, moe.GROUP_SUM2):
         check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=sum2)
+
+
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("E,G,keep", [(8, 4, 2), (8, 2, 1), (60, 5, 2), (64, 8, 3), (256, 8, 4), (400, 8, 2)])
+def test_finite_biases_of_the_lowest_value_in_group_sums(E, G, keep, k, score):
+    """A finite bias of the lowest value takes its expert's group down with it where the expert is one
+    of the group's two largest; -inf leaves the expert out of the sum."""
+    g = torch.Generator().manual_seed(E + k)
+    l, _ = draw(48, E, E)
+    size = E // G
+    for least in (torch.finfo(torch.float32).min, LOW, -1e38):
+        b = torch.randn(E, generator=g) * 0.05
+        for grp in range(0, G, 2):                   # all but one expert of every second group
+            b[grp * size + 1:(grp + 1) * size] = least
+        b[G // 2 * size] = -math.inf
+        check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
+        b[-1] = -least                               # and a largest one
+        check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
