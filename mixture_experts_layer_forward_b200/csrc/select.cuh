@@ -363,8 +363,7 @@ __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biase
         if (!((two ? v2 : v1) > -SEL_EDGE)) return v1 >= SEL_EDGE ? v1 : -SEL_LOW;
         return two && v1 < SEL_EDGE ? v1 + v2 : v1;
     }
-    if (!(v1 > -SEL_EDGE)) return v1;
-    return sel_score(a.sigmoid, v1, m, inv) + (v2 > -SEL_EDGE ? sel_score(a.sigmoid, v2, m, inv) : 0.0f);
+    return sel_score(a.sigmoid, v1, m, inv) + (v2 > -SEL_NONE ? sel_score(a.sigmoid, v2, m, inv) : 0.0f);
 }
 
 // Threads per block and blocks per SM (the launch fills the SMs once).
@@ -463,6 +462,10 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(v[i], -INFINITY), SEL_FAR);
             }
+        } else if (sums) { // a live logit has a score, if of 0, that counts for its group
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+                v[i] = v[i] > -INFINITY ? fminf(fmaxf(v[i], -SEL_LOW), SEL_FAR) : -SEL_FAR;
         } else { // the order of the logits: below -SEL_EDGE sel_exact settles what is live
 #pragma unroll
             for (int i = 0; i < EPT; ++i) v[i] = fminf(fmaxf(v[i], -SEL_FAR), SEL_FAR);

@@ -523,3 +523,21 @@ def test_finite_biases_of_the_lowest_value_in_group_sums(E, G, keep, k, score):
         check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
         b[-1] = -least                               # and a largest one
         check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
+
+
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,G,keep", [(8, 4, 2), (60, 5, 3), (64, 8, 4), (256, 8, 5), (400, 8, 3)])
+def test_groups_whose_scores_are_zero(E, G, keep, dtype, score):
+    """Without a bias: a live group whose scores are 0 in 64 bits (logits of -1000 or the lowest value)
+    equals another one, and comes before a masked one."""
+    g = torch.Generator().manual_seed(E)
+    l, _ = draw(48, E, E, dtype)
+    kinds = torch.tensor([0.0, -1000.0, torch.finfo(dtype).min, LOW, -math.inf])
+    for t in range(48):
+        pick = torch.randint(0, 5, (G,), generator=g)
+        pick[t % G] = 0
+        base = kinds[pick].repeat_interleave(E // G)
+        l[t] = torch.where(base == 0, l[t].float(), base).to(dtype)
+    for k in (1, 4):
+        check_rows(l, E, k, None, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
