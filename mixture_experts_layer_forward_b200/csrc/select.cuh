@@ -344,10 +344,11 @@ __device__ __forceinline__ int sel_id(float key)
     return (u >> 31) ? (int)(u & 0xffffu) : 1023 - (int)(u & 0xffffu);
 }
 
-// A score in 32 bits: the sigmoid, or exp(l - m) / sum with inv = 1 / sum.
+// A score in 32 bits: the sigmoid, or exp(l - m) / sum with inv = 1 / sum (the place in l's lowest
+// bits may take it past m, and a large one past what an exponential holds).
 __device__ __forceinline__ float sel_score(int sigmoid, float l, float m, float inv)
 {
-    return sigmoid ? sel_rcp(1.0f + sel_ex2(l * -SEL_LOG2E)) : sel_ex2((l - m) * SEL_LOG2E) * inv;
+    return sigmoid ? sel_rcp(1.0f + sel_ex2(l * -SEL_LOG2E)) : sel_ex2(fminf(l - m, 0.0f) * SEL_LOG2E) * inv;
 }
 
 // A group's value from its two largest keys (-SEL_FAR: none). Without a bias the keys are logits and

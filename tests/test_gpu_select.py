@@ -541,3 +541,17 @@ def test_groups_whose_scores_are_zero(E, G, keep, dtype, score):
         l[t] = torch.where(base == 0, l[t].float(), base).to(dtype)
     for k in (1, 4):
         check_rows(l, E, k, None, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
+
+
+@pytest.mark.parametrize("E,G,keep", [(8, 2, 1), (48, 6, 3), (60, 5, 2), (64, 8, 3), (256, 8, 4), (400, 8, 2)])
+def test_group_sums_of_logits_whose_steps_are_large(E, G, keep):
+    """Softmax without a bias: logits of 1e9 and 1e30, equal in several groups. What a key loses to its
+    place in the lane is then more than an exponential can carry."""
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(48, E, generator=g)
+    for t in range(48):
+        top = (1e30, 1.0000001e30, 1e9, 1.00000006e9, 3e7)[t % 5]
+        at = torch.randperm(G, generator=g)[:1 + t % G] * (E // G) + torch.randint(0, E // G, (1 + t % G,), generator=g)
+        l[t, at] = top
+    for k in (1, 2):
+        check_rows(l, E, k, None, score=moe.SCORE_SOFTMAX, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
