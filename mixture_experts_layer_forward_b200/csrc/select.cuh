@@ -367,6 +367,16 @@ __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biase
     return sel_score(a.sigmoid, v1, m, inv) + (v2 > -SEL_NONE ? sel_score(a.sigmoid, v2, m, inv) : 0.0f);
 }
 
+// What a group's value may be off by beyond its scores' own bounds, relative to its keys, not to their
+// sum: the two of a biased sum may cancel. (The sums with the biases, the keys' sum, this bound's and the
+// values' difference round by 2^-24 each: together SEL_TOL_KEY.)
+__device__ __forceinline__ float sel_group_error(const SelectArgs &a, bool biased, float tol_key, float gv,
+                                                 float v1, float v2)
+{
+    const bool sum = biased && a.sum2 && v2 > -SEL_EDGE;
+    return sum ? tol_key * fabsf(v1) + tol_key * fabsf(v2) : tol_key * fabsf(gv);
+}
+
 // Threads per block and blocks per SM (the launch fills the SMs once).
 __host__ __device__ constexpr int sel_threads(int lpt, int ept) { return ept == 32 ? 128 : 256; }
 __host__ __device__ constexpr int sel_blocks(int lpt, int ept)
@@ -536,11 +546,11 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
             const float gv = sel_group_value(a, BIASED, v1, v2, m, inv);
             const bool st = sel_group_stays(gv, a.groups, a.keep, lane);
             const uint32_t stay = __ballot_sync(0xffffffffu, st);
-            const float lo = sel_min_of<LPT>(st ? gv : SEL_FAR);
-            const float hi = sel_max_of<LPT>(!st && lane < a.groups ? gv : -SEL_FAR);
+            const float ge = sel_group_error(a, BIASED, SEL_TOL_KEY, gv, v1, v2);
+            const float lo = sel_min_of<LPT>(st ? gv - ge : SEL_FAR);
+            const float hi = sel_max_of<LPT>(!st && lane < a.groups ? gv + ge : -SEL_FAR);
             // (a lost group that stays while another lost one does not is as close as can be)
-            if ((BIASED || sums) && hi > -SEL_NONE && !(lo - hi > 2.0f * tol + SEL_TOL_KEY * (fabsf(lo) + fabsf(hi))))
-                bad = true;
+            if ((BIASED || sums) && hi > -SEL_NONE && !(lo - hi > 2.0f * tol)) bad = true;
 #pragma unroll
             for (int i = 0; i < EPT; ++i)
                 if (!((stay >> min((e0 + i) / a.gsz, 31)) & 1u)) v[i] = -SEL_FAR;
@@ -596,9 +606,11 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
             const int rank = rank_of(gv); // every lane takes part, its group real or not
             bool st = in && rank < a.keep;
             if (!EXACT || sums) {
-                const float lo = sel_min_of<LPT>(st ? gv : SEL_FAR), hi = sel_max_of<LPT>(in && !st ? gv : -SEL_FAR);
-                const bool close = hi > -SEL_NONE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) +
-                                                                     TOL_KEY * (fabsf(lo) + fabsf(hi)) + SEL_TOL_ZERO);
+                const float ge = sel_group_error(a, BIASED, TOL_KEY, gv, v1, v2);
+                const float lo = sel_min_of<LPT>(st ? gv - ge : SEL_FAR);
+                const float hi = sel_max_of<LPT>(in && !st ? gv + ge : -SEL_FAR);
+                const bool close =
+                    hi > -SEL_NONE && !(lo - hi > (BIASED || sums ? 2.0f * tol : 0.0f) + SEL_TOL_ZERO);
                 if (__any_sync(0xffffffffu, close)) {
                     // the groups' values again in 64 bits, from each lane's two largest (which are its two
                     // largest in 64 bits too, or the token goes to sel_exact)

@@ -555,3 +555,22 @@ def test_group_sums_of_logits_whose_steps_are_large(E, G, keep):
         l[t, at] = top
     for k in (1, 2):
         check_rows(l, E, k, None, score=moe.SCORE_SOFTMAX, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
+
+
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+@pytest.mark.parametrize("E,G,keep", [(8, 4, 1), (60, 5, 2), (64, 8, 3), (256, 8, 4), (400, 8, 2)])
+def test_group_sums_of_opposite_biases(E, G, keep, score):
+    """The two largest keys of a group may cancel: its value is then small and as exact as 64 bits make
+    it, not as 32 bits make the keys."""
+    g = torch.Generator().manual_seed(E)
+    size = E // G
+    l = torch.randn(64, E, generator=g)
+    live = torch.zeros(E, dtype=torch.bool)
+    b = torch.zeros(E)
+    for grp in range(G):                             # two live experts a group, biases +v and -v
+        v = float(10 ** (2 + 4 * torch.rand(1, generator=g)))
+        live[grp * size] = live[grp * size + size - 1] = True
+        b[grp * size], b[grp * size + size - 1] = v, -v
+    l[:, ~live] = -math.inf
+    for k in (1, 2):
+        check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
