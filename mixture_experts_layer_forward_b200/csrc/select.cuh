@@ -63,6 +63,7 @@ constexpr float SEL_FAR = 3.0e38f;
 constexpr float SEL_NONE = 2.97e38f;
 constexpr float SEL_LOW = 2.95e38f;
 constexpr float SEL_EDGE = 2.9e38f;
+constexpr float SEL_BIG = 1.0e38f; // a biased sum with a key at or beyond this: sel_exact
 
 struct SelectArgs {
     const void *logits; // [T, E], row stride ld (elements)
@@ -352,17 +353,16 @@ __device__ __forceinline__ float sel_score(int sigmoid, float l, float m, float 
 }
 
 // A group's value from its two largest keys (-SEL_FAR: none). Without a bias the keys are logits and
-// a sum is formed of their scores (the order is the same). A sum with a live expert's key at -SEL_LOW
-// is lost, as that key is: -SEL_LOW. (One with a key beyond SEL_EDGE is that key, which wins and sends
-// the token to sel_exact.)
+// a sum is formed of their scores (the order is the same). bad: a sum that 32 bits may not hold, or one
+// with a clamped key.
 __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biased, float v1, float v2,
-                                                 float m, float inv)
+                                                 float m, float inv, bool &bad)
 {
     if (!a.sum2 || !(v1 > -SEL_NONE)) return v1;
     if (biased) {
-        const bool two = v2 > -SEL_NONE;
-        if (!((two ? v2 : v1) > -SEL_EDGE)) return v1 >= SEL_EDGE ? v1 : -SEL_LOW;
-        return two && v1 < SEL_EDGE ? v1 + v2 : v1;
+        if (!(v2 > -SEL_NONE)) return v1;
+        if (!(v1 < SEL_BIG && v2 > -SEL_BIG)) bad = true;
+        return v1 + v2;
     }
     return sel_score(a.sigmoid, v1, m, inv) + (v2 > -SEL_NONE ? sel_score(a.sigmoid, v2, m, inv) : 0.0f);
 }
@@ -373,7 +373,7 @@ __device__ __forceinline__ float sel_group_value(const SelectArgs &a, bool biase
 __device__ __forceinline__ float sel_group_error(const SelectArgs &a, bool biased, float tol_key, float gv,
                                                  float v1, float v2)
 {
-    const bool sum = biased && a.sum2 && v2 > -SEL_EDGE;
+    const bool sum = biased && a.sum2 && v2 > -SEL_NONE;
     return sum ? tol_key * fabsf(v1) + tol_key * fabsf(v2) : tol_key * fabsf(gv);
 }
 
@@ -543,13 +543,13 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
                     v1 = fmaxf(v1, x);
                 }
             __syncwarp();
-            const float gv = sel_group_value(a, BIASED, v1, v2, m, inv);
+            const float gv = sel_group_value(a, BIASED, v1, v2, m, inv, bad);
             const bool st = sel_group_stays(gv, a.groups, a.keep, lane);
             const uint32_t stay = __ballot_sync(0xffffffffu, st);
             const float ge = sel_group_error(a, BIASED, SEL_TOL_KEY, gv, v1, v2);
             const float lo = sel_min_of<LPT>(st ? gv - ge : SEL_FAR);
             const float hi = sel_max_of<LPT>(!st && lane < a.groups ? gv + ge : -SEL_FAR);
-            // (a lost group that stays while another lost one does not is as close as can be)
+            // (two groups at the clamp are as close as can be)
             if ((BIASED || sums) && hi > -SEL_NONE && !(lo - hi > 2.0f * tol)) bad = true;
 #pragma unroll
             for (int i = 0; i < EPT; ++i)
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(sel_threads(LPT, EPT), sel_blocks(LPT, EPT))
                 v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
                 v1 = fmaxf(v1, o1);
             }
-            const float gv = sel_group_value(a, BIASED, v1, v2, m, inv);
+            const float gv = sel_group_value(a, BIASED, v1, v2, m, inv, bad);
             // the group's rank: its lanes compare with the groups c, c + lanes, ... and add up
             auto rank_of = [&](auto x) {
                 int rank = 0;

@@ -574,3 +574,22 @@ def test_group_sums_of_opposite_biases(E, G, keep, score):
     l[:, ~live] = -math.inf
     for k in (1, 2):
         check_rows(l, E, k, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
+
+
+@pytest.mark.parametrize("score", [moe.SCORE_SOFTMAX, moe.SCORE_SIGMOID])
+@pytest.mark.parametrize("E,G,keep", [(8, 4, 2), (16, 4, 2), (60, 5, 3), (64, 8, 4), (256, 8, 4), (400, 8, 4)])
+def test_group_sums_beyond_32_bits(E, G, keep, score):
+    """The sum of two finite keys may be larger than a float, or small again: 64 bits order the groups,
+    also against a group with nothing left."""
+    g = torch.Generator().manual_seed(E)
+    size = E // G
+    kinds = torch.tensor([1.2e38, 2e38, 2.8e38, -1.2e38, -2e38, -2.5e38, -2.8e38, -3.2e38, 0.25, 0.0])
+    for it in range(12):
+        l = torch.full((24, E), -math.inf)
+        b = kinds[torch.randint(3 if it % 3 else 0, 10, (E,), generator=g)]
+        for t in range(24):                          # one to three live experts a group, or none
+            for grp in range(G):
+                at = grp * size + torch.randperm(size, generator=g)[:int(torch.randint(0, 4, (1,), generator=g))]
+                l[t, at] = torch.randn(len(at), generator=g)
+            l[t, t % E] = 0.5
+        check_rows(l, E, 1 + it % 2, b, score=score, n_group=G, top_group=keep, group_score=moe.GROUP_SUM2)
