@@ -130,9 +130,19 @@ __device__ __forceinline__ float lin_gelu_gate(float z, float z2)
 }
 __device__ __forceinline__ float lin_silu(float z) { return z * lin_sigmoid(z); }
 __device__ __forceinline__ float lin_gelu(float z) { return z * lin_gelu_gate(z, z * z); }
-// s + z s (1 - s) w', w' = 2 sqrt(2 / pi) (1 + 3 * 0.044715 z^2)
+// z within +-lim; a NaN stays one
+__device__ __forceinline__ float lin_within(float z, float lim)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(lim));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-lim));
+    return r;
+}
+// s + z s (1 - s) w', w' = 2 sqrt(2 / pi) (1 + 3 * 0.044715 z^2). At 30 the gate s is 0 or 1 to the last
+// bit; further out the products would overflow against it (0 times infinity).
 __device__ __forceinline__ float lin_gelu_grad(float z)
 {
+    z = lin_within(z, 30.0f);
     const float z2 = z * z, s = lin_gelu_gate(z, z2);
     return s * fmaf(z * (1.0f - s), fmaf(3.0f * LIN_GK * LIN_GC2, z2, LIN_GC2), 1.0f);
 }

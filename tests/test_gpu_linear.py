@@ -370,3 +370,22 @@ def test_offsets_past_32_bits():
     moe.moe_linear_backward(q, x[-m:], W, zs, res[-m:], dxs, None, None, ws)
     assert moe.moe_get_device_status(ws) == 0
     assert torch.equal(dx[-m:], dxs)
+
+
+def test_gelu_gradient_far_out():
+    """The derivative is 0 and 1 where the gate is shut and open, whatever the size of z; a NaN stays
+    one. One row: dbias is dz itself, unrounded."""
+    far = [6.0, 9.0, 12.0, 30.0, 31.0, 1e4, 1e13, 1e14, 1e18, 2e19, 1e20, 1e30, 1e37, 3e38]
+    z = torch.tensor([v for f in far for v in (f, -f)] + [float("nan"), 0.0, 0.5, -0.5], dtype=BF)[None].cuda()
+    n = z.shape[1]
+    p = moe.Linear.make(1, n, 8, act=GELU)
+    ws = torch.empty(moe.moe_linear_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
+    dy, db = torch.ones(1, n, dtype=BF, device="cuda"), torch.empty(n, device="cuda")
+    x, W = torch.ones(1, 8, dtype=BF, device="cuda"), torch.ones(8, n, dtype=BF, device="cuda")
+    moe.moe_linear_backward(p, x, W, z, dy, None, None, db, ws)
+    nan = torch.isnan(z[0])
+    assert torch.equal(torch.isnan(db), nan)
+    z64 = z[0].double()
+    z64 = torch.where(z64.abs() > 100, z64.sign() * 100, z64)        # 0 or 1 to the last bit from 10 on
+    ref = grad64(GELU, z64, torch.ones_like(z64), n)
+    assert ((db.double() - ref).abs() <= 2.0 ** -19)[~nan].all()
