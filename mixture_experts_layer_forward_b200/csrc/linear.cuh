@@ -928,9 +928,10 @@ __global__ void __launch_bounds__(256, ACT == 0 ? 3 : 5) linear_dz_kernel(const 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (GATED) {
+                // the gate's factors first: 0 where it is shut, so that no product overflows before them
                 const float s = lin_sigmoid(g[i]);
-                const float du = d[i] * g[i] * s;
-                d[i] = d[i] * u[i] * s * fmaf(g[i], 1.0f - s, 1.0f);
+                const float du = d[i] * (g[i] * s);
+                d[i] *= u[i] * (s * fmaf(g[i], 1.0f - s, 1.0f));
                 u[i] = du;
                 su[i] += du;
             } else if (ACT == 1) {

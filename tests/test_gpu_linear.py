@@ -389,3 +389,22 @@ def test_gelu_gradient_far_out():
     z64 = torch.where(z64.abs() > 100, z64.sign() * 100, z64)        # 0 or 1 to the last bit from 10 on
     ref = grad64(GELU, z64, torch.ones_like(z64), n)
     assert ((db.double() - ref).abs() <= 2.0 ** -19)[~nan].all()
+
+
+def test_swiglu_gradient_of_large_values():
+    """A shut gate's gradients are 0 although dy times the gate's or up's value would overflow."""
+    g = torch.tensor([-1e30, -1e30, -3e38, -3e38, -2e20, 5.0, 200.0], dtype=BF)
+    u = torch.tensor([2.0, 1e30, 3.0, 1e38, -1e30, 1e20, -1e20], dtype=BF)
+    dy = torch.tensor([1e10, 1e10, 1e30, -1e30, 1e25, 1e10, 1e10], dtype=BF)
+    pad = lambda t: torch.cat([t, torch.zeros(1, dtype=BF)])
+    g, u, dy = pad(g), pad(u), pad(dy)
+    p = moe.Linear.make(1, 8, 8, act=SWIGLU)
+    z = torch.cat([g, u])[None].cuda()
+    ws = torch.empty(moe.moe_linear_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
+    db = torch.empty(16, device="cuda")
+    x, W = torch.ones(1, 8, dtype=BF, device="cuda"), torch.ones(8, 16, dtype=BF, device="cuda")
+    moe.moe_linear_backward(p, x, W, z, dy[None].cuda(), None, None, db, ws)
+    ref = grad64(SWIGLU, z.double().cpu(), dy.double()[None], 8)[0]
+    # the derivative's fast forms: 2^-19 of dy and the other factor, where the gate is not shut
+    fast = 2.0 ** -19 * torch.cat([dy * u, dy * g]).double().abs() * (torch.cat([g, g]) > -100)
+    assert ((db.double().cpu() - ref).abs() <= fast + 1e-30).all(), db
