@@ -406,5 +406,6 @@ def test_swiglu_gradient_of_large_values():
     moe.moe_linear_backward(p, x, W, z, dy[None].cuda(), None, None, db, ws)
     ref = grad64(SWIGLU, z.double().cpu(), dy.double()[None], 8)[0]
     # the derivative's fast forms: 2^-19 of dy and the other factor, where the gate is not shut
-    fast = 2.0 ** -19 * torch.cat([dy * u, dy * g]).double().abs() * (torch.cat([g, g]) > -100)
+    d64 = dy.double()
+    fast = 2.0 ** -19 * torch.cat([d64 * u.double(), d64 * g.double()]).abs() * (torch.cat([g, g]) > -100)
     assert ((db.double().cpu() - ref).abs() <= fast + 1e-30).all(), db
