@@ -635,7 +635,9 @@ MOE_API moe_status moe_route_noalloc(const moe_problem *p, const moe_bf16 *x, co
                                      void *stream);
 
 /* Test hook for the bounded device waits: the timeout, in nanoseconds, that every
- * bounded wait of later launches uses (default 2e9; values <= 0 restore the default).
+ * bounded wait of later launches uses (default 2e9; values <= 0 restore the default; the
+ * waits of moe_linear_* last at least 1e8, so that a block's copies and products in flight
+ * have always landed before it leaves).
  * Returns the previous value. Not thread-safe; meant for tests. */
 MOE_API int64_t moe_set_wait_timeout_ns(int64_t ns);
 

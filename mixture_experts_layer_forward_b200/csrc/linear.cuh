@@ -62,6 +62,10 @@ __host__ __device__ constexpr int smem_bytes(int bn, bool split)
 // tensor core adds to an accumulator by truncation, about 2^-26 of it a step of 16: 3.8e-6 over
 // K = 7168, 5e-7 over 512)
 constexpr int PROMOTE_K = 512;
+// Least limit of a wait, whatever moe_set_wait_timeout_ns asks for. Copies and products in flight take
+// microseconds to land, so a block that gives up never leaves before its own have; and block 0, the first
+// to be set up, has cleared the status word long before another block's wait can run out and record it.
+constexpr int64_t LEAST_WAIT_NS = 100000000;
 } // namespace lin
 
 struct LinearArgs {
@@ -83,7 +87,7 @@ struct LinearArgs {
     int full;             // 256-column tiles: those from this one on are worked as two halves
     int *status;
     int clear_status;     // block 0 clears the status word (the call's first launch with waits)
-    int64_t timeout_ns;
+    int64_t timeout_ns;   // at least lin::LEAST_WAIT_NS
 };
 
 __device__ __forceinline__ void lin_load_bias8(const float *bias, float (&b)[8])
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     const int tc = a.act == 0 ? BN / 2 : BN;
     const int run = PROMOTE ? lin::PROMOTE_K / lin::bk(BN) : a.k_blocks;
     order_wait();
-    if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
+    if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait has run out yet (LEAST_WAIT_NS)
         a.status[0] = DEV_OK;
         a.status[1] = 0;
     }
@@ -721,7 +725,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     float *park = reinterpret_cast<float *>(p.smem);
     const LinPark lay(BN, S, gated);
     order_wait();
-    if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait can have run out yet
+    if (a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) { // no wait has run out yet (LEAST_WAIT_NS)
         a.status[0] = DEV_OK;
         a.status[1] = 0;
     }

@@ -284,7 +284,7 @@ cudaError_t launch_linear(const void *A, int64_t lda, const void *B, int64_t ldb
     a.group_m = 16;
     a.splits = p.splits;
     a.a_rows = std::min(lin::BM, (a.M + 7) / 8 * 8);
-    a.timeout_ns = g_timeout_ns.load();
+    a.timeout_ns = std::max<int64_t>(g_timeout_ns.load(), lin::LEAST_WAIT_NS);
     // a last wave of at most half the SMs' tiles is worked in halves
     const int tiles = a.m_tiles * a.n_tiles, rest = tiles % sms;
     a.full = tiles > sms && 2 * rest <= sms ? tiles - rest : tiles;

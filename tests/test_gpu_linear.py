@@ -409,3 +409,18 @@ def test_swiglu_gradient_of_large_values():
     d64 = dy.double()
     fast = 2.0 ** -19 * torch.cat([d64 * u.double(), d64 * g.double()]).abs() * (torch.cat([g, g]) > -100)
     assert ((db.double().cpu() - ref).abs() <= fast + 1e-30).all(), db
+
+
+def test_the_shortest_wait_limit_still_finishes():
+    """The dense product's waits have a least limit of their own, so that copies and products in flight
+    are always waited for: a limit of one nanosecond changes nothing."""
+    for M, K, N, act, plan in ((300, 2056, 264, SWIGLU, (256, 0)), (64, 4096, 520, IDENT, (128, 4))):
+        moe.moe_set_linear_plan(*plan)
+        d = make(M, K, N, act, False, 3)
+        p = moe.Linear.make(M, N, K, act=act)
+        prev = moe.moe_set_wait_timeout_ns(1)
+        try:
+            check_forward(p, d, True, True, True)
+            check_backward(p, d)
+        finally:
+            moe.moe_set_wait_timeout_ns(prev)
