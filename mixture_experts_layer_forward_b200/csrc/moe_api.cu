@@ -591,7 +591,7 @@ cudaError_t launch_dispatch(const moe_problem *p, const Layout &L, const int32_t
     if (err != cudaSuccess) return err;
     if (nchunk > 0) {
         dispatch_place_kernel<<<nchunk, DISPATCH_CHUNK, (size_t)E * DISPATCH_WORDS * 4, st>>>(
-            topk_idx, topk_w, T, E, k, o.chunk, o.poff, o.gather_idx, o.inv_pos, o.row_w, n_rows);
+            topk_idx, topk_w, T, E, k, o.chunk, o.poff, o.gather_idx, o.inv_pos, o.row_w, status, n_rows);
     }
     return cudaGetLastError();
 }

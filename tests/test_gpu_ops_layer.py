@@ -206,3 +206,24 @@ def test_block_forward_and_backward():
     cg.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first, (out, dx, dxr, dWg, dW1, dW2)))
+
+
+@pytest.mark.parametrize("T", [300, 40])
+@pytest.mark.parametrize("k", [16, 17, 20, 32])
+def test_routed_layer_reports_an_expert_given_twice_among_many(T, k):
+    """However many experts a token has."""
+    cfg = synth.LayerConfig("many", T=T, H=128, F=128, E=40, k=k)
+    inp = synth.make_inputs(cfg, seed=5, device="cuda")
+    p = moe.Problem.from_config(cfg)
+    g = torch.Generator().manual_seed(k)
+    idx = torch.stack([torch.randperm(40, generator=g)[:k] for _ in range(T)]).to(I32).cuda()
+    w = torch.rand(T, k, device="cuda")
+    ws = zeros(moe.moe_backward_workspace_size(p))
+    out, dx = empty(T, 128), empty(T, 128)
+    dw, dW1, dW2 = empty(T, k, dtype=F32), torch.empty_like(inp["W1"]), torch.empty_like(inp["W2"])
+    for want in (0, -6):
+        moe.moe_forward_routed(p, inp["x"], idx, w, inp["W1"], inp["W2"], out, ws)
+        assert moe.moe_get_device_status(ws) == want
+        moe.moe_backward_routed(p, inp["x"], idx, w, inp["W1"], inp["W2"], out, dx, dw, dW1, dW2, ws)
+        assert moe.moe_get_device_status(ws) == want
+        idx[T - 3, k - 1] = idx[T - 3, 2]
