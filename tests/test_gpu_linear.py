@@ -424,3 +424,50 @@ def test_the_shortest_wait_limit_still_finishes():
             check_backward(p, d)
         finally:
             moe.moe_set_wait_timeout_ns(prev)
+
+
+FP32_PLANS = [(128, 0), (64, 1), (64, 2), (64, 4), (64, 8), (128, 1), (128, 2), (128, 4), (128, 8)]
+
+
+@pytest.mark.parametrize("plan", FP32_PLANS)
+@pytest.mark.parametrize("M,K,N", [(5, 1032, 72), (200, 1544, 328), (140, 4104, 136)])
+def test_every_plan_with_fp32_outputs_and_long_k(M, K, N, plan):
+    """fp32 outputs of more than 512 values of k, whose runs of 512 are summed in registers; the last
+    run short, some parts of the split without a whole one."""
+    moe.moe_set_linear_plan(*plan)
+    for act, nk in ((IDENT, False), (IDENT, True), (SWIGLU, False), (SWIGLU, True), (GELU, False)):
+        d = make(M, K, N, act, nk, M + K, F32)
+        p = moe.Linear.make(M, N, K, act=act, w_layout=moe.W_NK if nk else moe.W_KN, out_dtype=F32)
+        check_forward(p, d, True, True, True)
+
+
+@pytest.mark.parametrize("nk", [False, True])
+@pytest.mark.parametrize("M,K,N,act", [(1304, 1544, 4360, IDENT), (1304, 1096, 2056, SWIGLU), (2600, 600, 2056, GELU)])
+def test_fp32_outputs_of_several_tiles_a_block(M, K, N, act, nk):
+    """More than two tiles a block of the persistent form: its runs and barriers carry on from one tile to
+    the next."""
+    moe.moe_set_linear_plan(128, 0)
+    d = make(M, K, N, act, nk, 77, F32)
+    p = moe.Linear.make(M, N, K, act=act, w_layout=moe.W_NK if nk else moe.W_KN, out_dtype=F32)
+    check_forward(p, d, True, True, True)
+
+
+@pytest.mark.parametrize("plan", [(128, 0), (128, 2), (64, 1), (64, 8)])
+@pytest.mark.parametrize("M,K,N", [(200, 7168, 264), (130, 16384, 72)])
+def test_fp32_sums_of_one_sign(M, K, N, plan):
+    """Products of one sign, where truncation adds up. A run of 512 takes 32 steps of 16 products; a step
+    loses at most 2^-23 of the accumulator, which grows evenly over the run: at most 16.5 * 2^-23 of the
+    run's sum (with the spread of the runs' growth 18), 2.2e-6. The runs are added in registers (and the
+    parts of a split): K / 512 + 8 roundings, each 2^-24 of a sum that grows evenly, so half of them. One
+    accumulator over all of K loses 2.9e-5 at K = 7168, 7.5e-5 at 16384."""
+    moe.moe_set_linear_plan(*plan)
+    g = torch.Generator().manual_seed(K)
+    x, W = torch.rand(M, K, generator=g).to(BF).cuda(), torch.rand(K, N, generator=g).to(BF).cuda()
+    p = moe.Linear.make(M, N, K, out_dtype=F32)
+    y, ws = torch.empty(M, N, device="cuda"), torch.empty(256, dtype=torch.uint8, device="cuda")
+    moe.moe_linear_forward(p, x, W, None, None, y, ws)
+    assert moe.moe_get_device_status(ws) == 0
+    ref = x.double() @ W.double()
+    tol = 18 * 2.0 ** -23 + (K / 512 + 10) * 2.0 ** -25
+    err = ((y.double() - ref) / ref).abs().max()
+    assert err <= tol, float(err)
