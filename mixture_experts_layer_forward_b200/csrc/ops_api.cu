@@ -75,16 +75,17 @@ cudaError_t launch_select(const SelectArgs &a, cudaStream_t st)
 template <typename LT, bool BIASED> cudaError_t launch_select_wide(const SelectArgs &a, cudaStream_t st)
 {
     // Four tokens per warp where they fit (k <= 8, E <= 256, groups of whole lanes) and there are
-    // enough of them: fewer instructions a token, but longer chains a lane. Measured, a warp each
-    // against eight lanes each: E = 256 (8 groups, bias) T = 4096 7.1 / 8.2 us, 8192 9.8 / 10.3,
-    // 16384 16.1 / 14.4; E = 128 (bias) 5.2 / 6.0, 7.1 / 7.0, 10.1 / 8.9; E = 64 3.6 / 4.5, 6.1 / 4.8,
-    // 8.7 / 6.4; E = 8 T = 1024 2.2 / 2.2, 2048 2.5 / 2.3, 4096 3.0 / 2.3, 16384 5.8 / 2.9.
+    // enough of them: fewer instructions a token, but longer chains a lane. Measured on the device, a
+    // warp each against eight lanes each: E = 256 (8 groups, bias) T = 4096 7.6 / 8.2 us, 8192 10.0 / 9.8,
+    // 16384 16.8 / 14.0; E = 128 (the same) 6.2 / 7.0, 8.5 / 8.0, 13.6 / 10.5; E = 64 3.9 / 4.8, 5.6 / 4.6,
+    // 8.8 / 6.2; E = 32 T = 2048 2.8 / 3.2, 4096 3.6 / 3.7, 8192 5.2 / 4.0; E = 16 2.8 / 3.0, 3.6 / 3.1,
+    // 5.2 / 3.3; E = 8 2.6 / 2.6, 3.2 / 2.6, 4.5 / 2.7.
     int ept = 1;
     while (ept * 8 < a.E) ept *= 2;
     const int lanes = a.gsz / ept;
     const bool fits = a.k <= 8 && a.E <= 256 &&
                       (a.groups == 1 || (a.gsz % ept == 0 && (lanes & (lanes - 1)) == 0));
-    if (fits && a.T >= (a.E <= 32 ? 2048 : 8192)) {
+    if (fits && a.T >= (a.E <= 16 ? 4096 : 8192)) {
         switch (ept) {
         case 1: return launch_select<8, 1, LT, BIASED>(a, st);
         case 2: return launch_select<8, 2, LT, BIASED>(a, st);
@@ -330,8 +331,10 @@ LinearBwdLayout linear_bwd_layout(const moe_linear *p, const LinearDims &d)
 {
     LinearBwdLayout L{};
     L.need_dz = p->act != MOE_ACT_IDENTITY || p->out_dtype == MOE_DTYPE_F32;
-    // one wave of blocks over the column blocks of a 148-SM part, five per SM (SwiGLU three: more
-    // registers), whole groups of 8 rows; 4096 x 6400 GELU: 31.0 us, against 36.9 with six per SM
+    // one wave of blocks over the column blocks of 148 SMs, five per SM (SwiGLU three: more registers),
+    // whole groups of 8 rows; 4096 x 6400 GELU: 31.0 us, against 36.9 with six per SM. Not the current
+    // device's count: the workspace's size does not depend on a device, and sums are added in the same
+    // order on each
     const int64_t cb = (p->N + 255) / 256;
     int64_t chunks = std::max<int64_t>(1, 148 * (p->act == MOE_ACT_SWIGLU ? 3 : 5) / cb);
     const int64_t groups = std::max<int64_t>(1, ((int64_t)p->M + 7) / 8);
