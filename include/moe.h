@@ -454,7 +454,8 @@ MOE_API moe_status moe_backward(const moe_problem *p, const moe_bf16 *x, const m
 /* The layer with a supplied routing: moe_forward without its router, for routings made by
  * moe_route_select or by the caller. topk_idx [T, k] int32, topk_w [T, k] fp32; a token's
  * experts are distinct. Dispatch, experts and combine as in moe_forward (the same launches,
- * less the router's; never the whole-layer launch). An id outside [0, E) or an expert given twice
+ * less the router's; never the whole-layer launch; one more that checks the ids where top_k > 16 and
+ * T > 256). An id outside [0, E) or an expert given twice
  * for one token is reported as MOE_ERR_DEVICE_BAD_INDEX through moe_get_device_status; an id outside
  * [0, E) contributes nothing to its token. shared: NULL, or the shared expert of
  * moe_forward_shared (workspace moe_workspace_size_shared). p->gate is not used. */

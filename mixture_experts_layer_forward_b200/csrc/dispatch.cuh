@@ -23,7 +23,6 @@ namespace moe {
 
 constexpr int DISPATCH_CHUNK = 256; // tokens per chunk (one thread per token)
 constexpr int DISPATCH_WORDS = DISPATCH_CHUNK / 32;
-constexpr int DISPATCH_PAIR_K = 16; // up to this top_k a token's ids are compared pair by pair
 constexpr int M_TILE = 128;
 
 // Workspace-resident bookkeeping written by the scan and read by the GEMMs.
@@ -58,9 +57,8 @@ __global__ void __launch_bounds__(DISPATCH_CHUNK)
             } else {
                 record_status(status, DEV_BAD_INDEX, 1);
             }
-            // a token's experts must be distinct (checked here for the usual small k, for a larger one
-            // by dispatch_place_kernel's bitmap)
-            if (k <= DISPATCH_PAIR_K) {
+            // a token's experts must be distinct (checked for the usual small k)
+            if (k <= 16) {
                 for (int j2 = 0; j2 < j; ++j2)
                     if (topk_idx[(size_t)t * k + j2] == e) record_status(status, DEV_BAD_INDEX, 2);
             }
@@ -293,7 +291,7 @@ __global__ void __launch_bounds__(DISPATCH_CHUNK)
                           int T, int E, int k, const int32_t *__restrict__ chunk_base,
                           const int32_t *__restrict__ padded_offsets,
                           int32_t *__restrict__ gather_idx, int32_t *__restrict__ inv_pos,
-                          float *__restrict__ row_w, int *status, const int *__restrict__ n_rows)
+                          float *__restrict__ row_w, const int *__restrict__ n_rows)
 {
     extern __shared__ uint32_t bits[];
     for (int i = threadIdx.x; i < E * DISPATCH_WORDS; i += blockDim.x) bits[i] = 0u;
@@ -306,11 +304,7 @@ __global__ void __launch_bounds__(DISPATCH_CHUNK)
     if (t < T) {
         for (int j = 0; j < k; ++j) {
             const int e = topk_idx[(size_t)t * k + j];
-            if (e < 0 || e >= E) continue;
-            if (k <= DISPATCH_PAIR_K)
-                atomicOr(&bits[e * DISPATCH_WORDS + word], bit);
-            else if (atomicOr(&bits[e * DISPATCH_WORDS + word], bit) & bit)
-                record_status(status, DEV_BAD_INDEX, 2);
+            if (e >= 0 && e < E) atomicOr(&bits[e * DISPATCH_WORDS + word], bit);
         }
     }
     __syncthreads();

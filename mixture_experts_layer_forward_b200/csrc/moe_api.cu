@@ -23,6 +23,7 @@
 #include "ptx.cuh"
 #include "route.cuh"
 #include "route_filter.cuh"
+#include "routed.cuh"
 #include "gemm_narrow.cuh"
 
 namespace moe {
@@ -591,8 +592,19 @@ cudaError_t launch_dispatch(const moe_problem *p, const Layout &L, const int32_t
     if (err != cudaSuccess) return err;
     if (nchunk > 0) {
         dispatch_place_kernel<<<nchunk, DISPATCH_CHUNK, (size_t)E * DISPATCH_WORDS * 4, st>>>(
-            topk_idx, topk_w, T, E, k, o.chunk, o.poff, o.gather_idx, o.inv_pos, o.row_w, status, n_rows);
+            topk_idx, topk_w, T, E, k, o.chunk, o.poff, o.gather_idx, o.inv_pos, o.row_w, n_rows);
     }
+    return cudaGetLastError();
+}
+
+// A supplied routing's check for an expert given twice, where the dispatch makes none (behind it on the
+// stream: the dispatch clears the status word).
+cudaError_t launch_routed_distinct(const moe_problem *p, const Layout &L, const int32_t *topk_idx, int *status,
+                                   cudaStream_t st)
+{
+    if (p->top_k <= ROUTED_PAIR_K || L.nchunk <= 1) return cudaSuccess;
+    routed_distinct_kernel<<<(unsigned)(((int64_t)p->T + 7) / 8), 256, 0, st>>>(topk_idx, p->T, p->E, p->top_k,
+                                                                               status);
     return cudaGetLastError();
 }
 
@@ -1037,6 +1049,7 @@ moe_status forward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16 
         // with the routing supplied the dispatch clears the status word (and checks the ids)
         if (e == cudaSuccess)
             e = launch_dispatch(p, L, topk_idx, topk_w, d, status, given ? 1 : 0, st, n_rows);
+        if (e == cudaSuccess && given) e = launch_routed_distinct(p, L, topk_idx, status, st);
         if (e == cudaSuccess && xperm) e = launch_gather(p, x, d.gather_idx, d.meta, x_perm, st);
         if (e == cudaSuccess) e = record(events, n_events, 2, st);
     }
@@ -1312,6 +1325,7 @@ moe_status backward_impl(const moe_problem *p, const moe_bf16 *x, const moe_bf16
                          at<float>(ws, L.logits), status, st, &fb);
     // with the routing supplied the dispatch clears the status word (and checks the ids)
     if (e == cudaSuccess) e = launch_dispatch(p, L, topk_idx, topk_w, d, status, given ? 1 : 0, st);
+    if (e == cudaSuccess && given) e = launch_routed_distinct(p, L, topk_idx, status, st);
     if (e == cudaSuccess) e = launch_gather(p, x, d.gather_idx, d.meta, x_perm, st);
 
     GemmArgs g{};
