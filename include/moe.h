@@ -497,7 +497,11 @@ MOE_API moe_status moe_backward_routed(const moe_problem *p, const moe_bf16 *x, 
  *             bias) counts as the lowest key; masked experts come after every other expert of the
  *             groups that stay, by id, and weigh 0, so every token has top_k distinct ids;
  *   weights   w_j = scale * s_j / sum of the selected s (renorm != 0; 0 where all are masked), or
- *             scale * s_j.
+ *             scale * s_j, in 32-bit arithmetic (a few 2^-24 of the value; the softmax over all
+ *             logits, renorm == 0, sums fast exponentials: up to 4e-6).
+ * Any finite logit is live, the type's lowest value too: its score is 0 and its bias may win.
+ * Tokens whose keys 32 bits cannot order take longer: a batch of 16384 tokens and 256 experts takes
+ * 13 us with random fp32 logits, 39 us with bf16 logits and a bias of 0, 103 us with equal logits.
  * Supported: E <= 1024, top_k <= 32, n_group <= 32 dividing E, top_k <= top_group * E / n_group,
  * 0 < scale < 3e38. ld: elements from one row of logits to the next (0: E). */
 #define MOE_SCORE_SOFTMAX 0
@@ -536,6 +540,11 @@ MOE_API moe_status moe_route_select_backward(const moe_select *s, const void *lo
  *   bias [C] fp32 or NULL (16-byte aligned); residual [M, N] bf16 or NULL; y [M, N] of out_dtype;
  *   z [M, C] bf16 or NULL: the pre-activation, for moe_linear_backward.
  * fp32 accumulation and epilogue, one rounding of y (and one of z). N % 8 == 0, K % 8 == 0; M any.
+ * The tensor core truncates what it adds to an accumulator. bf16 outputs (the gradients too) are
+ * summed in one: off by up to 2.9e-5 of the sum of the products' sizes at K = 7168, growing with K,
+ * against a rounding of up to 3.9e-3. fp32 outputs add an accumulator of 512 values of K at a time to
+ * sums in registers: 1e-6. SiLU, GELU and their derivatives are formed with the fast 2^x and 1 / x
+ * (2^-19 of the value, and of dy times the other factor).
  * ld*: elements from one row to the next (0: dense), each row start 16-byte aligned. residual may be y
  * when both are bf16 with the same strides. */
 #define MOE_W_KN 0
@@ -564,8 +573,9 @@ MOE_API moe_status moe_linear_forward(const moe_linear *p, const moe_bf16 *x, co
 /* dz = dy act'(z); dx [M, K] = dz W^T, dW = x^T dz in W's layout (both dense, bf16), dbias [C] fp32 =
  * column sums of dz. dy [M, N] of out_dtype with row stride ldy. Any of dx, dW, dbias may be NULL (not
  * wanted), not all. z: as moe_linear_forward wrote it (not used, may be NULL, for MOE_ACT_IDENTITY). The
- * residual's gradient is dy itself. dz is rounded to bf16 for the products; dbias sums it unrounded,
- * in fp32, in a fixed order. Up to four launches. */
+ * residual's gradient is dy itself. dz is rounded to bf16 for the products, an fp32 dy too (the
+ * gradients' error is then 0.0023 of their norm, against 0.0017 of their own rounding alone);
+ * dbias sums it unrounded, in fp32, in a fixed order. Up to four launches. */
 MOE_API moe_status moe_linear_backward(const moe_linear *p, const moe_bf16 *x, const moe_bf16 *W,
                                        const moe_bf16 *z, const void *dy, moe_bf16 *dx, moe_bf16 *dW,
                                        float *dbias, void *ws, size_t ws_bytes, void *stream);

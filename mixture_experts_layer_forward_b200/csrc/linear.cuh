@@ -26,11 +26,11 @@
 // Every wait is bounded as in the other kernels here: a block that gives up records the
 // timeout, waits for its copies and products in flight, frees its TMEM and leaves.
 //
-// Measured (M x K x N): 4096^3 101 us, 1360 TFLOP/s (0.83 of the measured burst rate: the tensor
-// pipe is busy 71 to 75% of the launch); 8192 x 4096 x 2 * 14336 SwiGLU 1.25 to 1.40 ms, by the power cap (0.94
-// to 1.09 of the sustained rate); 4096 x 7168 x 256 fp32 22 us, bound by what an SM takes from L2 (64 KB per 128 x
-// 128 x 128 step, 130 GB/s); 64 x 7168 x 2 * 2048 SwiGLU 16 us, 1 x 4096 x 4096 9.6 us (59 and 34 MB of W at 6.5
-// TB/s: 9 and 5 us, the rest start, reduction and end of the launch). Row strides that are not a multiple
+// Measured (M x K x N), calls back to back: 4096^3 101 us, 1360 TFLOP/s (0.83 of the measured burst rate: the
+// tensor pipe is busy 71 to 75% of the launch); 8192 x 4096 x 2 * 14336 SwiGLU 1.47 ms under the power cap (0.94 of
+// the sustained rate), 1.28 ms cool; 4096 x 7168 x 256 fp32 24.2 us, bound by what an SM takes from L2 (64 KB per
+// 128 x 128 x 128 step, 130 GB/s); 64 x 7168 x 2 * 2048 SwiGLU 16.3 us, 1 x 4096 x 4096 9.6 us (59 and 34 MB of W
+// at 6.5 TB/s: 9 and 5 us, the rest start, reduction and end of the launch). Row strides that are not a multiple
 // of 128 bytes cost up to half as much again while operands come from L2 (1003 x 1160 x 2568: 13.6 us of products
 // against 9.1 at K = 1152).
 #pragma once

@@ -172,7 +172,7 @@ struct LinearPlan {
 };
 
 // Tile width and k split by an estimate of one launch's time in microseconds, from measurements at
-// 1 to 8192 rows: a 64-value block of k of a 128 x BN tile takes 0.30, 0.19, 0.165 (BN = 256, 128,
+// 1 to 8192 rows (device time): a 64-value block of k of a 128 x BN tile takes 0.30, 0.19, 0.165 (BN = 256, 128,
 // 64); a persistent launch pays start and last epilogue once (7.0, 5.5), a split one per tile, more of
 // it for more rows and splits. Measured, the choice against the best of the others: 1 x 4096 x 4096
 // (M x K x N) 9.7 (128 columns, 4 splits) / 10.4; 64 x 7168 x 2 * 2048 SwiGLU 16.1 (128, 4) / 19.2;

@@ -14,17 +14,20 @@
 // The selection is the one that keys in 64 bits give. Keys are first formed in 32 bits with the
 // fast exponential, whose distance from the 64-bit key is bounded (SEL_TOL_*). Where every
 // decision of a token was clear of that bound the 32-bit selection is the 64-bit one. Otherwise
-// (about 3 tokens in 1000 of random logits) the groups' values, or the k + 1 winners' keys, are
+// (about 5 tokens in 1000 of random fp32 logits) the groups' values, or the k + 1 winners' keys, are
 // formed again in 64 bits and ordered by them; and where that does not settle it (ties around the
 // last place, masked or infinite winners) the warp selects from scratch with 64-bit keys
-// (sel_exact: 10 us for a token, against 1 us).
-// Measured: 16384 tokens, 256 experts in 8 groups, fp32, bias: 16 us (2.6 us of bytes at the
-// measured copy rate); 8192 tokens, 64 experts, bf16: 3.7 us; one token: 2.9 us.
+// (sel_exact: some 10 us for a token, and the launch waits for it).
+// Measured on the device: 16384 tokens, 256 experts in 8 groups, fp32, bias: 13 to 15 us (2.6 us of
+// bytes at the measured copy rate), and 18 to 21 in one random batch of eight, where a token selects
+// from scratch. Ties: bf16 logits with a bias of 0 (five of six warps settle winners in 64 bits, one
+// token in 42 selects from scratch) 39 us, all logits equal 103 us. 8192 tokens, 64 experts, bf16:
+// 3.8 us; one token: 3.7 us, 14 with all logits equal.
 //
 // LPT lanes per token (a warp, or eight lanes: four tokens per warp); lane i owns the EPT
-// consecutive experts from i * EPT. With 256 experts a row is 1 KB and the work is 660 warp
-// instructions a token with a warp each, 350 with eight lanes, so the kernel is bound by
-// instructions and their latency, not bytes, and is built to spend few per key:
+// consecutive experts from i * EPT. With 256 experts a row is 1 KB and a token of a batch takes 386
+// warp instructions with eight lanes, so the kernel is bound by instructions and their latency, not
+// bytes, and is built to spend few per key:
 //   - a key carries its place in the lane in its lowest log2(EPT) mantissa bits (counted in the
 //     bound), so a key and its expert sort as one float: min and max, nothing else;
 //   - each lane sorts its keys once (19 exchanges for 8); a round of the top-k is then one

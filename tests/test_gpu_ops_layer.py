@@ -227,3 +227,30 @@ def test_routed_layer_reports_an_expert_given_twice_among_many(T, k):
         moe.moe_backward_routed(p, inp["x"], idx, w, inp["W1"], inp["W2"], out, dx, dw, dW1, dW2, ws)
         assert moe.moe_get_device_status(ws) == want
         idx[T - 3, k - 1] = idx[T - 3, 2]
+
+
+def test_router_of_a_number_of_experts_that_the_product_refuses():
+    """60 experts: the product makes 64 columns of logits, routing reads the first 60 of each row, and the
+    gradient's last 4 columns are zeros."""
+    T, H, E, k = 70, 128, 60, 4
+    g = torch.Generator("cuda").manual_seed(4)
+    x = torch.randn(T, H, device="cuda", generator=g).to(BF)
+    Wg = torch.zeros(H, 64, dtype=BF, device="cuda")
+    Wg[:, :E] = torch.randn(H, E, device="cuda", generator=g).to(BF) * H ** -0.5
+    with pytest.raises(moe.MoeError):
+        moe.moe_linear_forward(moe.Linear.make(T, E, H, out_dtype=F32), x, Wg[:, :E].contiguous(), None, None,
+                               empty(T, E, dtype=F32), zeros(256))
+    lin, sel = moe.Linear.make(T, 64, H, out_dtype=F32), moe.Select.make(T, E, k)
+    ws = zeros(moe.moe_linear_backward_workspace_size(lin))
+    logits, idx, w = empty(T, 64, dtype=F32), empty(T, k, dtype=I32), empty(T, k, dtype=F32)
+    moe.moe_linear_forward(lin, x, Wg, None, None, logits, ws)
+    moe.moe_route_select(sel, logits[:, :E], None, idx, w)
+    own_i, own_w = empty(T, k, dtype=I32), empty(T, k, dtype=F32)
+    moe.moe_route_select(sel, logits[:, :E].contiguous(), None, own_i, own_w)
+    assert torch.equal(idx, own_i) and torch.equal(w, own_w) and int(idx.max()) < E
+    dl, dW, dx = empty(T, E, dtype=F32), empty(H, 64), empty(T, H)
+    moe.moe_route_select_backward(sel, logits[:, :E], idx, torch.ones_like(w).cumsum(1), dl)
+    dy = torch.nn.functional.pad(dl, (0, 64 - E))
+    moe.moe_linear_backward(lin, x, Wg, None, dy, dx, dW, None, ws)
+    assert moe.moe_get_device_status(ws) == 0
+    assert (dW[:, E:] == 0).all() and not (dW[:, :E] == 0).all()
